@@ -107,6 +107,18 @@ _SIGNATURES = {
     "gpt2op_lm_head_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "gpt2op_lm_head_ce_workspace": (_SZ, [_I, _I]),
     "gpt2op_lm_head_ce": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _P]),
+    "gpt2_token_logps": (_I, [_P, _P, _P, _I32, _I32, _P]),
+    "gpt2_fwd_bwd_policy": (_I, [_P, _P, _P, _P, _P, _P, _P, _I32, _F, _F, _F, _F, _P, _FP]),
+    "gpt2_fwd_bwd_preference": (_I, [_P, _P, _P, _P, _I32, _I, _I, _F, _F, _P, _FP]),
+    "gpt2_muon_workspace": (_SZ, [ctypes.POINTER(Config)]),
+    "gpt2_clip_muon": (_I, [_P, _I32, _F, _P, _SZ, _FP]),
+    "gpt2op_token_logps": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "gpt2op_policy_loss": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _F, _F, _P, _P]),
+    "gpt2op_preference_loss_workspace": (_SZ, [_I, _I]),
+    "gpt2op_preference_loss": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _P, _SZ,
+                                    _P, _P]),
+    "gpt2op_orthogonalize_workspace": (_SZ, [_I, _I, _I]),
+    "gpt2op_orthogonalize": (_I, [_P, _I, _I64, _P, _I64, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "gpt2op_embedding_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "gpt2op_embedding_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "gpt2op_wait_selftest": (_I, [_I64, _P, _P]),
@@ -165,8 +177,56 @@ def schedule_lr(cfg: Config, step: int) -> float:
     return lib().gpt2_schedule_lr(ctypes.byref(cfg), step)
 
 
+def muon_workspace(cfg: Config) -> int:
+    """Bytes of workspace GPT2.clip_muon needs for `cfg`."""
+    return lib().gpt2_muon_workspace(ctypes.byref(cfg))
+
+
 def num_params(cfg: Config, padded: bool = False) -> int:
     return lib().gpt2_num_params(ctypes.byref(cfg), 1 if padded else 0)
+
+
+PREFERENCE_KINDS = {"sigmoid": 0, "squared": 1}
+
+
+def _kind(name: str) -> int:
+    if name not in PREFERENCE_KINDS:
+        raise ValueError(f"kind {name!r}: one of {sorted(PREFERENCE_KINDS)}")
+    return PREFERENCE_KINDS[name]
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _rows_of(T: int, tokens) -> int:
+    n = tokens.numel()
+    if n == 0 or n % T:
+        raise ValueError(f"tokens: {n} positions are not whole sequences of {T}")
+    return n
+
+
+def _want(dtype: str, numel, device=None, optional: bool = False, **tensors):
+    """Check device tensors against a type, an element count (None: any), contiguity and
+    a device (None: the first one's); returns the device."""
+    for name, t in tensors.items():
+        if t is None:
+            if optional:
+                continue
+            raise ValueError(f"{name} is required")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a device tensor is needed")
+        if str(t.dtype) != "torch." + dtype:
+            raise ValueError(f"{name}: {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: not contiguous")
+        if numel is not None and t.numel() != numel:
+            raise ValueError(f"{name}: {t.numel()} elements, not {numel}")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name}: on {t.device}, not {device}")
+    return device
 
 
 @dataclass
@@ -215,6 +275,48 @@ class GPT2:
         check(lib().gpt2_fwd_bwd(self.h, _ptr(tokens), _ptr(targets),
                                  ctypes.byref(out) if want_loss else None), "gpt2_fwd_bwd")
         return out.value if want_loss else None
+
+    def token_logps(self, tokens, targets, logps, ignore_index: int = -1):
+        """logps (device fp32, tokens' shape) = the targets' log-probabilities, 0 where ignored."""
+        n = _rows_of(self.T, tokens)
+        dev = _want("int32", n, tokens=tokens, targets=targets)
+        _want("float32", n, dev, logps=logps)
+        check(lib().gpt2_token_logps(self.h, _ptr(tokens), _ptr(targets), n // self.T, ignore_index, _ptr(logps)),
+              "gpt2_token_logps")
+
+    def fwd_bwd_policy(self, tokens, targets, old_logp, adv, ref_logp=None, weight=None, ignore_index: int = -1,
+                       clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0,
+                       logps=None, want_loss: bool = False):
+        """One micro-step on the clipped policy loss; per-position inputs are device fp32 [B, T]."""
+        n = self.B * self.T
+        dev = _want("int32", n, tokens=tokens, targets=targets)
+        _want("float32", n, dev, old_logp=old_logp, adv=adv)
+        _want("float32", n, dev, True, ref_logp=ref_logp, weight=weight, logps=logps)
+        out = ctypes.c_float()
+        check(lib().gpt2_fwd_bwd_policy(self.h, _ptr(tokens), _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(adv),
+                                        _ptr(weight), ignore_index, clip_low, clip_high, kl_coef, scale, _ptr(logps),
+                                        ctypes.byref(out) if want_loss else None), "gpt2_fwd_bwd_policy")
+        return out.value if want_loss else None
+
+    def fwd_bwd_preference(self, tokens, targets, ref_logp=None, ignore_index: int = -1, kind: str = "sigmoid",
+                           average: bool = False, beta: float = 0.1, smoothing: float = 0.0, seq_logps=None,
+                           want_loss: bool = False):
+        """One micro-step on the paired preference loss: sequences 2p (chosen) and 2p + 1 (rejected)."""
+        dev = _want("int32", self.B * self.T, tokens=tokens, targets=targets)
+        _want("float32", self.B, dev, True, ref_logp=ref_logp, seq_logps=seq_logps)
+        out = ctypes.c_float()
+        check(lib().gpt2_fwd_bwd_preference(self.h, _ptr(tokens), _ptr(targets), _ptr(ref_logp), ignore_index,
+                                            _kind(kind), 1 if average else 0, beta, smoothing, _ptr(seq_logps),
+                                            ctypes.byref(out) if want_loss else None), "gpt2_fwd_bwd_preference")
+        return out.value if want_loss else None
+
+    def clip_muon(self, step: int, workspace, momentum: float = 0.95, want_norm: bool = False):
+        """The optimizer step with orthogonalised momentum for the blocks' 2-D weights;
+        workspace: a device tensor of at least muon_workspace(cfg) bytes."""
+        out = ctypes.c_float()
+        check(lib().gpt2_clip_muon(self.h, step, momentum, _ptr(workspace), _nbytes(workspace),
+                                   ctypes.byref(out) if want_norm else None), "gpt2_clip_muon")
+        return out.value if want_norm else None
 
     def clip_adamw(self, step: int, want_norm: bool = False):
         out = ctypes.c_float()
@@ -505,3 +607,127 @@ def embedding_bwd(tokens, dx, dwte, dwpe, V, stream=None):
     C = dwte.shape[1]
     check(lib().gpt2op_embedding_bwd(_ptr(tokens), _ptr(dx), _ptr(dwte), _ptr(dwpe), B, T, C, V,
                                      _s(stream)), "gpt2op_embedding_bwd")
+
+
+# The post-training operators check their tensors, and run on the tensors' device.
+
+class _on:
+    """The tensors' device as the current one, where it is not, and its stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError(f"stream on {self.stream.device}, tensors on {device}")
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _logits_shape(logits, V):
+    if logits.dim() != 2:
+        raise ValueError(f"logits: [rows, padded ids] are needed, not {tuple(logits.shape)}")
+    N, Vp = logits.shape
+    if not 0 < V <= Vp:
+        raise ValueError(f"V = {V} real ids of {Vp} columns")
+    return N, Vp
+
+
+def token_logps(logits, targets, logps, V, err, ignore_index=-1, stream=None):
+    """logps = each row's log-probability of its target over the V real ids (0 where ignored)."""
+    N, Vp = _logits_shape(logits, V)
+    dev = _want("bfloat16", None, logits=logits)
+    _want("int32", N, dev, targets=targets)
+    _want("int32", None, dev, err=err)
+    _want("float32", N, dev, logps=logps)
+    with _on(dev, stream) as s:
+        check(lib().gpt2op_token_logps(_ptr(logits), _ptr(targets), _ptr(logps), N, V, Vp, ignore_index, _ptr(err), s),
+              "gpt2op_token_logps")
+
+
+def policy_loss(logits, targets, old_logp, adv, dlogits, logps, losses, V, err, ref_logp=None, weight=None,
+                ignore_index=-1, clip_low=0.2, clip_high=0.2, kl_coef=0.0, dscale=1.0, stream=None):
+    """Clipped policy loss with a KL term and its gradient over the logits.
+
+    dlogits: None (losses alone), the logits (in place) or a tensor of their shape;
+    logps may be None; ref_logp is required with kl_coef > 0."""
+    N, Vp = _logits_shape(logits, V)
+    dev = _want("bfloat16", None, logits=logits)
+    _want("bfloat16", N * Vp, dev, True, dlogits=dlogits)
+    _want("int32", N, dev, targets=targets)
+    _want("int32", None, dev, err=err)
+    _want("float32", N, dev, old_logp=old_logp, adv=adv, losses=losses)
+    _want("float32", N, dev, True, ref_logp=ref_logp, weight=weight, logps=logps)
+    with _on(dev, stream) as s:
+        check(lib().gpt2op_policy_loss(_ptr(logits), _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(adv),
+                                       _ptr(weight), _ptr(dlogits), _ptr(logps), _ptr(losses), N, V, Vp, ignore_index,
+                                       clip_low, clip_high, kl_coef, dscale, _ptr(err), s), "gpt2op_policy_loss")
+
+
+def preference_loss_workspace(N, P):
+    return lib().gpt2op_preference_loss_workspace(N, P)
+
+
+def preference_loss(logits, targets, seq_start, dlogits, logps, seq_logps, losses, V, workspace, err, ref_logp=None,
+                    ignore_index=-1, kind="sigmoid", average=False, beta=0.1, smoothing=0.0, dscale=1.0, stream=None):
+    """Paired preference loss and its gradient over the logits; seq_start int32 [2P + 1],
+    sequence 2p chosen and 2p + 1 rejected. dlogits as in policy_loss; seq_logps may be None."""
+    N, Vp = _logits_shape(logits, V)
+    P = (seq_start.numel() - 1) // 2
+    if P < 1 or seq_start.numel() != 2 * P + 1:
+        raise ValueError(f"seq_start: {seq_start.numel()} bounds are not 2P + 1")
+    dev = _want("bfloat16", None, logits=logits)
+    _want("bfloat16", N * Vp, dev, True, dlogits=dlogits)
+    _want("int32", N, dev, targets=targets)
+    _want("int32", None, dev, seq_start=seq_start, err=err)
+    _want("float32", N, dev, logps=logps)
+    _want("float32", P, dev, losses=losses)
+    _want("float32", 2 * P, dev, True, ref_logp=ref_logp, seq_logps=seq_logps)
+    _want("uint8", None, dev, workspace=workspace)
+    with _on(dev, stream) as s:
+        check(lib().gpt2op_preference_loss(_ptr(logits), _ptr(targets), _ptr(seq_start), _ptr(ref_logp), _ptr(dlogits),
+                                           _ptr(logps), _ptr(seq_logps), _ptr(losses), N, P, V, Vp, ignore_index,
+                                           _kind(kind), 1 if average else 0, beta, smoothing, dscale, _ptr(workspace),
+                                           workspace.numel(), _ptr(err), s), "gpt2op_preference_loss")
+
+
+def orthogonalize_workspace(batch, rows, cols):
+    return lib().gpt2op_orthogonalize_workspace(batch, rows, cols)
+
+
+def _matrices(name, t):
+    """(batch, rows, cols, elements between matrices) of contiguous [rows, cols] matrices."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name}: [rows, cols] or [batch, rows, cols], not {tuple(t.shape)}")
+    b, r, c = (1, *t.shape) if t.dim() == 2 else t.shape
+    if t.stride(-1) != 1 and c > 1 or t.stride(-2) != c and r > 1:
+        raise ValueError(f"{name}: the matrices are not contiguous")
+    return b, r, c, t.stride(0) if t.dim() == 3 and b > 1 else r * c
+
+
+def orthogonalize(x, out, workspace, err, steps=5, stream=None):
+    """out = the Newton-Schulz orthogonalisation of x: [rows, cols] or [batch, rows, cols]
+    (matrices may lie apart), x fp32 or bf16, out bf16."""
+    b, r, c, xs = _matrices("x", x)
+    ob, orows, oc, os_ = _matrices("out", out)
+    if (ob, orows, oc) != (b, r, c):
+        raise ValueError(f"out: {tuple(out.shape)}, x: {tuple(x.shape)}")
+    x_fp32 = str(x.dtype) == "torch.float32"
+    if not x_fp32 and str(x.dtype) != "torch.bfloat16":
+        raise ValueError(f"x: {x.dtype}, not float32 or bfloat16")
+    if str(out.dtype) != "torch.bfloat16":
+        raise ValueError(f"out: {out.dtype}, not bfloat16")
+    if not x.is_cuda or out.device != x.device:
+        raise ValueError(f"x on {x.device}, out on {out.device}: one GPU is needed")
+    _want("uint8", None, x.device, workspace=workspace)
+    _want("int32", None, x.device, err=err)
+    with _on(x.device, stream) as s:
+        check(lib().gpt2op_orthogonalize(_ptr(x), 1 if x_fp32 else 0, xs, _ptr(out), os_, b, r, c, steps,
+                                         _ptr(workspace), workspace.numel(), _ptr(err), s), "gpt2op_orthogonalize")

@@ -30,6 +30,8 @@
 #include "gemm.cuh"
 #include "gemm2sm.cuh"
 #include "kernels.cuh"
+#include "muon.cuh"
+#include "posttrain.cuh"
 
 namespace {
 
@@ -524,9 +526,83 @@ int ln_fwd_m(gpt2_model* m, const bf16* x, int kw, int kb, int l, bf16* y, float
   return st;
 }
 
+// What follows the logits in place of the cross-entropy.
+struct LossSpec {
+  enum Kind { LOGPS, POLICY, PREFERENCE } kind;
+  pt::PolicyArgs policy;   // POLICY: the caller's inputs and scalars
+  pt::PairArgs pair;       // PREFERENCE: the caller's inputs and scalars
+  float* logps;            // LOGPS: one per position; POLICY: the same or null
+  int ignore_index;
+};
+
+// The loss of `spec` on the logits of `N` rows (`lse_part`: the logits GEMM's row
+// partials or null; `tgt_val`: the targets' logits where no logits are stored),
+// with its gradient over the logits for the training losses.
+int spec_loss(gpt2_model* m, const LossSpec& spec, const int32_t* tgt, int N, bf16* logits, const float2* lse_part,
+              const float* tgt_val, double* loss_acc) {
+  const Layout& y = m->lay;
+  const Dims& d = y.d;
+  cudaStream_t s = m->stream;
+  float* losses = m->at<float>(y.losses);
+  const int slots = lse_slots(d.Vp);
+  const size_t p = prof_begin(m);
+  int nl = 1, n_loss = 0;
+  const float* loss_src = losses;
+  double factor = 0.0;
+  if (spec.kind == LossSpec::POLICY) {
+    pt::PolicyArgs a = spec.policy;
+    a.logits = a.dlogits = logits;
+    a.targets = tgt; a.logps = spec.logps; a.losses = losses;
+    a.part = lse_part; a.slots = slots; a.V = d.V; a.Vp = d.Vp; a.ignore_index = spec.ignore_index;
+    a.err = m->err();
+    GPT2_TRY(pt::policy_loss(a, N, s));
+    n_loss = N;
+    factor = a.dscale;
+  } else {
+    pt::RowArgs r{};
+    r.logits = tgt_val ? nullptr : logits;
+    r.targets = tgt; r.part = lse_part; r.tgt_val = tgt_val; r.slots = slots; r.V = d.V; r.Vp = d.Vp;
+    r.ignore_index = spec.ignore_index; r.err = m->err();
+    r.logps = spec.kind == LossSpec::LOGPS ? spec.logps : losses;
+    // the row and pair scratch lives in the attention backward's per-query terms,
+    // which are free until that runs (32 bytes a row and head)
+    const int P = d.B / 2;
+    float2* stats = m->at<float2>(y.attD);
+    float* coef = reinterpret_cast<float*>(stats + d.N);
+    if (spec.kind == LossSpec::PREFERENCE) r.stats = stats;
+    GPT2_TRY(pt::row_logps(r, N, s));
+    if (spec.kind == LossSpec::PREFERENCE) {
+      pt::PairArgs a = spec.pair;
+      a.logps = losses; a.targets = tgt; a.seq_start = nullptr; a.seq_len = d.T; a.N = N; a.V = d.V;
+      a.ignore_index = spec.ignore_index; a.coef = coef; a.losses = coef + 2 * P; a.err = m->err();
+      launch_pdl(pt::pair_kernel, dim3(P), dim3(pt::kRowThreads), 0, s, a);
+      pt::PairGradArgs g{};
+      g.logits = g.dlogits = logits;
+      g.targets = tgt; g.stats = stats; g.coef = coef; g.n_seq = 2 * P; g.seq_len = d.T; g.V = d.V; g.Vp = d.Vp;
+      g.ignore_index = spec.ignore_index;
+      launch_pdl(pt::pair_grad_kernel, dim3(N), dim3(pt::kRowThreads), 0, s, g);
+      nl += 2;
+      n_loss = P;
+      loss_src = a.losses;
+      factor = a.dscale;
+    }
+  }
+  if (n_loss) {
+    launch_pdl(pt::scaled_loss_kernel, dim3(1), dim3(1024), 0, s, loss_src, n_loss, factor, (double)N, loss_acc,
+               &m->sc()->micro_loss);
+    ++nl;
+  }
+  const double part_bytes = lse_part ? (double)N * slots * 8.0 : 0.0;
+  const double row_bytes = spec.kind == LossSpec::LOGPS ? (lse_part ? 2.0 : 2.0 * d.Vp) : 4.0 * d.Vp;
+  prof_end(m, p, PC_CE, (double)N * row_bytes + part_bytes, nl);
+  return cudaGetLastError() == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
+}
+
 // Forward over `b` sequences; `train` keeps dlogits for the backward pass,
-// otherwise only losses are produced. Loss sum goes to *loss_acc.
-int forward(gpt2_model* m, const int32_t* tok, const int32_t* tgt, int b, bool train, double* loss_acc) {
+// otherwise only losses are produced. Loss sum goes to *loss_acc. With `spec` the
+// given loss takes the cross-entropy's place.
+int forward(gpt2_model* m, const int32_t* tok, const int32_t* tgt, int b, bool train, double* loss_acc,
+            const LossSpec* spec = nullptr) {
   const Layout& y = m->lay;
   const Dims& d = y.d;
   const int C = d.C, T = d.T, L = d.L;
@@ -612,6 +688,7 @@ int forward(gpt2_model* m, const int32_t* tok, const int32_t* tgt, int b, bool t
     }
     GPT2_TRY(run_gemm(m, c));
   }
+  if (spec) return spec_loss(m, *spec, tgt, (int)N, logits, lse_part, logits_free ? losses : nullptr, loss_acc);
   {
     const size_t p = prof_begin(m);
     GPT2_TRY(launch::softmax_ce(logits_free ? nullptr : logits, tgt, losses, (int)N, d.V, d.Vp, 1.0f / (float)N,
@@ -947,6 +1024,80 @@ int gpt2_fwd_bwd(gpt2_model* m, const int32_t* tokens, const int32_t* targets, f
   return GPT2_OK;
 }
 
+// The micro-step with `spec`'s loss in place of the cross-entropy.
+static int fwd_bwd_spec(gpt2_model* m, const int32_t* tokens, const int32_t* targets, const LossSpec& spec,
+                        float* loss_out) {
+  GPT2_TRY(forward(m, tokens, targets, m->lay.d.B, true, &m->sc()->loss_sum, &spec));
+  GPT2_TRY(backward(m, tokens));
+  m->n_micro += 1;
+  if (loss_out) {
+    GPT2_TRY(collect_device_error(m));
+    if (cudaMemcpy(loss_out, &m->sc()->micro_loss, sizeof(float), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return GPT2_ERR_CUDA;
+  }
+  return GPT2_OK;
+}
+
+// Scalars of the policy loss; a KL weight needs the reference, and without one the reference is not read.
+static bool policy_scalars(const float* ref_logp, float clip_low, float clip_high, float kl_coef, float scale,
+                           pt::PolicyArgs* a) {
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f && isfinite(clip_high))) return false;
+  if (!(kl_coef >= 0.f && isfinite(kl_coef)) || !isfinite(scale) || (kl_coef > 0.f && !ref_logp)) return false;
+  a->ref_logp = kl_coef > 0.f ? ref_logp : nullptr;
+  a->clip_low = clip_low; a->clip_high = clip_high; a->kl_coef = kl_coef; a->dscale = scale;
+  return true;
+}
+
+static bool pair_scalars(int kind, int average, float beta, float smoothing, float scale, pt::PairArgs* a) {
+  if (kind != GPT2_PREFERENCE_SIGMOID && kind != GPT2_PREFERENCE_SQUARED) return false;
+  if (!(beta > 0.f && isfinite(beta)) || !(smoothing >= 0.f && smoothing < 1.f) || !isfinite(scale)) return false;
+  if (kind == GPT2_PREFERENCE_SQUARED && smoothing != 0.f) return false;
+  a->kind = kind; a->average = average != 0; a->beta = beta; a->smoothing = smoothing; a->dscale = scale;
+  return true;
+}
+
+int gpt2_token_logps(gpt2_model* m, const int32_t* tokens, const int32_t* targets, int32_t batch, int32_t ignore_index,
+                     float* logps) {
+  if (!m || !tokens || !targets || batch <= 0 || !logps) return GPT2_ERR_ARG;
+  const Dims& d = m->lay.d;
+  LossSpec spec{};
+  spec.kind = LossSpec::LOGPS;
+  spec.ignore_index = ignore_index;
+  for (int b0 = 0; b0 < batch; b0 += d.B) {
+    const size_t at = (size_t)b0 * d.T;
+    spec.logps = logps + at;
+    GPT2_TRY(forward(m, tokens + at, targets + at, std::min(d.B, batch - b0), false, nullptr, &spec));
+  }
+  return GPT2_OK;
+}
+
+int gpt2_fwd_bwd_policy(gpt2_model* m, const int32_t* tokens, const int32_t* targets, const float* old_logp,
+                        const float* ref_logp, const float* adv, const float* weight, int32_t ignore_index,
+                        float clip_low, float clip_high, float kl_coef, float scale, float* logps, float* loss_out) {
+  LossSpec spec{};
+  if (!m || !tokens || !targets || !old_logp || !adv ||
+      !policy_scalars(ref_logp, clip_low, clip_high, kl_coef, scale, &spec.policy))
+    return GPT2_ERR_ARG;
+  spec.kind = LossSpec::POLICY;
+  spec.policy.old_logp = old_logp; spec.policy.adv = adv; spec.policy.weight = weight;
+  spec.logps = logps;
+  spec.ignore_index = ignore_index;
+  return fwd_bwd_spec(m, tokens, targets, spec, loss_out);
+}
+
+int gpt2_fwd_bwd_preference(gpt2_model* m, const int32_t* tokens, const int32_t* targets, const float* ref_logp,
+                            int32_t ignore_index, int kind, int average, float beta, float smoothing,
+                            float* seq_logps, float* loss_out) {
+  LossSpec spec{};
+  if (!m || !tokens || !targets || (m->lay.d.B & 1) ||
+      !pair_scalars(kind, average, beta, smoothing, 2.0f / (float)m->lay.d.B, &spec.pair))
+    return GPT2_ERR_ARG;
+  spec.kind = LossSpec::PREFERENCE;
+  spec.pair.ref_logp = ref_logp; spec.pair.seq_logps = seq_logps;
+  spec.ignore_index = ignore_index;
+  return fwd_bwd_spec(m, tokens, targets, spec, loss_out);
+}
+
 // Host-side form of element ranges: float4 ranges, validated against the layout
 // (each 64-element aligned, inside [0, P), at most Ranges4::kMax of them).
 static bool to_ranges4(const gpt2_model* m, const int64_t* ranges, int n, k::Ranges4* out) {
@@ -959,6 +1110,13 @@ static bool to_ranges4(const gpt2_model* m, const int64_t* ranges, int n, k::Ran
     out->end[r] = e / 4;
   }
   return true;
+}
+
+// Synchronises; the pre-clip norm of the last update, and any device error.
+static int read_grad_norm(gpt2_model* m, float* out) {
+  const int st = collect_device_error(m);
+  if (cudaMemcpy(out, &m->sc()->last_norm, sizeof(float), cudaMemcpyDeviceToHost) != cudaSuccess) return GPT2_ERR_CUDA;
+  return st;
 }
 
 // The update half of the step over the given ranges, with the norm finalised from
@@ -988,13 +1146,7 @@ static int clip_adamw_impl(gpt2_model* m, int32_t step, const k::Ranges4& rg, co
   if (cudaGetLastError() != cudaSuccess) return GPT2_ERR_CUDA;
   m->n_micro = 0;
   m->stepped = true;
-  if (grad_norm_out) {
-    const int st = collect_device_error(m);
-    if (cudaMemcpy(grad_norm_out, &m->sc()->last_norm, sizeof(float), cudaMemcpyDeviceToHost) != cudaSuccess)
-      return GPT2_ERR_CUDA;
-    return st;
-  }
-  return GPT2_OK;
+  return grad_norm_out ? read_grad_norm(m, grad_norm_out) : GPT2_OK;
 }
 
 int gpt2_clip_adamw(gpt2_model* m, int32_t step, float* grad_norm_out) {
@@ -1010,6 +1162,60 @@ int gpt2_clip_adamw(gpt2_model* m, int32_t step, float* grad_norm_out) {
   launch_pdl(k::sumsq_partial_kernel, dim3(kNormBlocks), dim3(512), 0, m->stream, m->grads(), all, part);
   prof_end(m, pr, PC_OPT, 4.0 * (double)y.P, 1);
   return clip_adamw_impl(m, step, all, part, kNormBlocks, false, grad_norm_out);
+}
+
+// The 2-D weights of the blocks: one batch per kind, its matrices a bucket apart
+// from the last block's to the first's.
+static const int kMuonKinds[] = {K_QKVW, K_ATTPROJW, K_FCW, K_FCPROJW};
+
+static size_t muon_workspace(const Layout& y) {
+  size_t most = 0;
+  for (int kk : kMuonKinds)
+    most = std::max(most, muon::update_workspace(y.d.L, y.kind[kk].rows, y.kind[kk].cols));
+  return most;
+}
+
+size_t gpt2_muon_workspace(const gpt2_config* cfg) {
+  Dims d;
+  if (!resolve(cfg, &d)) return 0;
+  Layout lay;
+  make_layout(d, &lay);
+  return muon_workspace(lay);
+}
+
+int gpt2_clip_muon(gpt2_model* m, int32_t step, float momentum, void* workspace, size_t ws_bytes,
+                   float* grad_norm_out) {
+  if (!m || step < 0 || !(momentum >= 0.f && momentum < 1.f)) return GPT2_ERR_ARG;
+  const Layout& y = m->lay;
+  const Dims& d = y.d;
+  if (d.L > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < muon_workspace(y)))
+    return GPT2_ERR_ARG;
+  if (m->n_micro == 0) return GPT2_ERR_STATE;
+  // the norm over everything; AdamW on the 1-D parameters and the embeddings
+  k::Ranges4 all{}, rest{};
+  all.n = 1;
+  all.end[0] = y.P / 4;
+  rest.n = 2;
+  rest.end[0] = y.P1 / 4;
+  rest.begin[1] = (d.L > 0 ? y.bucket_end[d.L - 1] : y.P1) / 4;
+  rest.end[1] = y.P / 4;
+  double* part = m->at<double>(y.norm_part);
+  size_t pr = prof_begin(m);
+  launch_pdl(k::sumsq_partial_kernel, dim3(kNormBlocks), dim3(512), 0, m->stream, m->grads(), all, part);
+  prof_end(m, pr, PC_OPT, 4.0 * (double)y.P, 1);
+  GPT2_TRY(clip_adamw_impl(m, step, rest, part, kNormBlocks, false, nullptr));
+  const float lr = (float)lr_at(m->cfg, step);
+  for (int kk : kMuonKinds) {
+    if (d.L == 0) break;
+    const int rows = y.kind[kk].rows, cols = y.kind[kk].cols;
+    const long first = m->off(kk, d.L - 1), stride = d.L > 1 ? m->off(kk, d.L - 2) - first : (long)rows * cols;
+    pr = prof_begin(m);
+    GPT2_TRY(muon::update(m->params() + first, m->pbf() + first, m->grads() + first, m->at<float>(y.adam_m) + first,
+                          stride, d.L, rows, cols, lr, momentum, m->cfg.weight_decay, &m->sc()->gscale, &m->sc()->skip,
+                          workspace, ws_bytes, m->err(), m->stream));
+    prof_end(m, pr, PC_OPT, 30.0 * (double)d.L * rows * cols, muon::kUpdateLaunches);
+  }
+  return grad_norm_out ? read_grad_norm(m, grad_norm_out) : GPT2_OK;
 }
 
 int gpt2_num_buckets(const gpt2_model* m) { return m ? (int)m->lay.bucket_end.size() : -1; }
@@ -1437,6 +1643,89 @@ int gpt2op_softmax_ce_masked(void* logits, const int32_t* targets, float* losses
   if (!logits || !targets || !losses || !dev_err || N <= 0 || ignore_index == INT_MIN) return GPT2_ERR_ARG;
   return launch::softmax_ce(static_cast<bf16*>(logits), targets, losses, N, V, Vp, dscale, 1, dev_err,
                             static_cast<cudaStream_t>(stream), ignore_index);
+}
+
+// dlogits: null, the logits themselves, or memory of its own
+static bool dlogits_ok(const void* logits, const void* dlogits, int N, int Vp) {
+  if (!dlogits || dlogits == logits) return true;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(logits), b = reinterpret_cast<uintptr_t>(dlogits);
+  const size_t bytes = (size_t)N * Vp * 2;
+  return pt::aligned16(dlogits) && (b >= a + bytes || a >= b + bytes);
+}
+
+int gpt2op_token_logps(const void* logits, const int32_t* targets, float* logps, int N, int V, int Vp, int ignore_index,
+                       int* dev_err, void* stream) {
+  if (!logits || !targets || !logps || !dev_err || !pt::logits_ok(logits, N, V, Vp)) return GPT2_ERR_ARG;
+  pt::RowArgs r{};
+  r.logits = static_cast<const bf16*>(logits);
+  r.targets = targets; r.logps = logps; r.V = V; r.Vp = Vp; r.ignore_index = ignore_index; r.err = dev_err;
+  return pt::row_logps(r, N, static_cast<cudaStream_t>(stream));
+}
+
+int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* old_logp, const float* ref_logp,
+                       const float* adv, const float* weight, void* dlogits, float* logps, float* losses, int N, int V,
+                       int Vp, int ignore_index, float clip_low, float clip_high, float kl_coef, float dscale,
+                       int* dev_err, void* stream) {
+  pt::PolicyArgs a{};
+  if (!logits || !targets || !old_logp || !adv || !losses || !dev_err || !pt::logits_ok(logits, N, V, Vp) ||
+      !dlogits_ok(logits, dlogits, N, Vp) || !policy_scalars(ref_logp, clip_low, clip_high, kl_coef, dscale, &a))
+    return GPT2_ERR_ARG;
+  a.logits = static_cast<const bf16*>(logits);
+  a.targets = targets; a.old_logp = old_logp; a.adv = adv; a.weight = weight;
+  a.dlogits = static_cast<bf16*>(dlogits);
+  a.logps = logps; a.losses = losses; a.V = V; a.Vp = Vp; a.ignore_index = ignore_index; a.err = dev_err;
+  return pt::policy_loss(a, N, static_cast<cudaStream_t>(stream));
+}
+
+size_t gpt2op_preference_loss_workspace(int N, int P) { return N > 0 && P > 0 ? pt::preference_workspace(N, P) : 0; }
+
+int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int32_t* seq_start, const float* ref_logp,
+                           void* dlogits, float* logps, float* seq_logps, float* losses, int N, int P, int V, int Vp,
+                           int ignore_index, int kind, int average, float beta, float smoothing, float dscale,
+                           void* workspace, size_t ws_bytes, int* dev_err, void* stream) {
+  pt::PairArgs a{};
+  if (!logits || !targets || !seq_start || !logps || !losses || !workspace || !dev_err || P <= 0 || P > (1 << 29) ||
+      !pt::logits_ok(logits, N, V, Vp) || !dlogits_ok(logits, dlogits, N, Vp) ||
+      !pair_scalars(kind, average, beta, smoothing, dscale, &a))
+    return GPT2_ERR_ARG;
+  if (ws_bytes < pt::preference_workspace(N, P) || (reinterpret_cast<uintptr_t>(workspace) & 7)) return GPT2_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float2* stats = static_cast<float2*>(workspace);
+  pt::RowArgs r{};
+  r.logits = static_cast<const bf16*>(logits);
+  r.targets = targets; r.logps = logps; r.stats = stats; r.seq_start = seq_start; r.n_seq = 2 * P; r.V = V; r.Vp = Vp;
+  r.ignore_index = ignore_index; r.err = dev_err;
+  GPT2_TRY(pt::row_logps(r, N, s));
+  a.logps = logps; a.targets = targets; a.seq_start = seq_start; a.ref_logp = ref_logp; a.seq_logps = seq_logps;
+  a.losses = losses; a.coef = reinterpret_cast<float*>(stats + N); a.N = N; a.V = V; a.ignore_index = ignore_index;
+  a.err = dev_err;
+  launch_pdl(pt::pair_kernel, dim3(P), dim3(pt::kRowThreads), 0, s, a);
+  if (dlogits) {
+    pt::PairGradArgs g{};
+    g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats; g.coef = a.coef;
+    g.dlogits = static_cast<bf16*>(dlogits);
+    g.n_seq = 2 * P; g.V = V; g.Vp = Vp; g.ignore_index = ignore_index;
+    launch_pdl(pt::pair_grad_kernel, dim3(N), dim3(pt::kRowThreads), 0, s, g);
+  }
+  return cudaGetLastError() == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
+}
+
+size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols) {
+  muon::Work w;
+  return muon::plan(batch, rows, cols, &w) ? w.total : 0;
+}
+
+int gpt2op_orthogonalize(const void* x, int x_fp32, int64_t x_stride, void* out, int64_t out_stride, int batch,
+                         int rows, int cols, int steps, void* workspace, size_t ws_bytes, int* dev_err, void* stream) {
+  if (!x || !out || !workspace || !dev_err) return GPT2_ERR_ARG;
+  if (rows <= 0 || cols <= 0 || batch <= 0) return GPT2_ERR_ARG;
+  if (batch > 1 && (x_stride < (int64_t)rows * cols || out_stride < (int64_t)rows * cols)) return GPT2_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bf16* o = static_cast<bf16*>(out);
+  return x_fp32 ? muon::orthogonalize(static_cast<const float*>(x), x_stride, o, out_stride, batch, rows, cols, steps,
+                                      workspace, ws_bytes, dev_err, s)
+                : muon::orthogonalize(static_cast<const bf16*>(x), x_stride, o, out_stride, batch, rows, cols, steps,
+                                      workspace, ws_bytes, dev_err, s);
 }
 
 int gpt2op_wait_selftest(int64_t limit_ns, int* dev_err, void* stream) {

@@ -60,6 +60,9 @@ typedef struct gpt2_model gpt2_model; /* opaque */
  * bf16 copy the tensor cores read, only through gpt2_state_device_ptr). */
 enum { GPT2_PARAMS = 0, GPT2_GRADS = 1, GPT2_ADAM_M = 2, GPT2_ADAM_V = 3, GPT2_WEIGHTS_BF16 = 4 };
 
+/* The paired preference losses. */
+enum { GPT2_PREFERENCE_SIGMOID = 0, GPT2_PREFERENCE_SQUARED = 1 };
+
 /* Bytes of device memory the caller must provide to gpt2_create for this
  * configuration (fp32 params, grads, m, v; bf16 weight copy; saved activations;
  * logits; workspaces). Returns 0 for an invalid configuration. Supported shapes:
@@ -221,6 +224,60 @@ int gpt2_grad_sumsq(gpt2_model* model, const int64_t* ranges, int n_ranges, doub
  * gpt2_clip_adamw. */
 int gpt2_clip_adamw_ranges(gpt2_model* model, int32_t step, const int64_t* ranges, int n_ranges,
                            const double* dev_sumsq, float* grad_norm_out);
+
+/* ---- post-training ------------------------------------------------------
+ * The micro-step with another loss over the logits, and the optimizer step with
+ * orthogonalised momentum. The pages train their adapter by supervision alone
+ * (the adaptation paragraph); these have no counterpart there. The losses are
+ * the ones of gpt2step_ops.h, where their formulas stand. Positions whose target
+ * equals ignore_index (prompts, padding) are left out; every other target must
+ * be an id in [0, vocab_real). */
+
+/* Log-probabilities of the targets under the model: forward only, asynchronous.
+ * tokens_dev / targets_dev int32 [batch, seq_len] (batch may exceed micro_batch),
+ * logps_dev fp32 [batch, seq_len], 0 where the target is ignore_index. They are
+ * the old and reference log-probabilities that the calls below take. */
+int gpt2_token_logps(gpt2_model* model, const int32_t* tokens_dev, const int32_t* targets_dev, int32_t batch,
+                     int32_t ignore_index, float* logps_dev);
+
+/* gpt2_fwd_bwd with the clipped policy loss (gpt2op_policy_loss) in place of
+ * the cross-entropy: the micro-batch's loss is scale * the sum of the positions'
+ * losses (scale: e.g. 1 / kept positions), its gradient is ADDED to the gradient
+ * buffers, and gpt2_clip_adamw or gpt2_clip_muon averages over the micro-steps
+ * as ever. old_logp, ref_logp (NULL with kl_coef 0), adv, weight (may be NULL):
+ * device fp32 [micro_batch, seq_len]. logps_dev (may be NULL) receives the
+ * positions' log-probabilities; gpt2_token_losses then returns their losses. */
+int gpt2_fwd_bwd_policy(gpt2_model* model, const int32_t* tokens_dev, const int32_t* targets_dev,
+                        const float* old_logp_dev, const float* ref_logp_dev, const float* adv_dev,
+                        const float* weight_dev, int32_t ignore_index, float clip_low, float clip_high,
+                        float kl_coef, float scale, float* logps_dev, float* loss_out);
+
+/* gpt2_fwd_bwd with the paired preference loss (gpt2op_preference_loss), mean
+ * over the pairs: sequences 2p and 2p + 1 of the micro-batch (micro_batch even)
+ * are pair p's chosen and rejected ones. ref_logp_dev fp32 [micro_batch]: the
+ * reference's log-probability of each sequence (summed, or with `average` mean,
+ * over its kept positions), NULL for none; seq_logps_dev fp32 [micro_batch] (may
+ * be NULL) receives the model's. gpt2_token_losses then returns the positions'
+ * log-probabilities. */
+int gpt2_fwd_bwd_preference(gpt2_model* model, const int32_t* tokens_dev, const int32_t* targets_dev,
+                            const float* ref_logp_dev, int32_t ignore_index, int kind, int average, float beta,
+                            float smoothing, float* seq_logps_dev, float* loss_out);
+
+/* Optimizer step with orthogonalised momentum for the blocks' 2-D weights (the
+ * four per block); the 1-D parameters and the embeddings take gpt2_clip_adamw's
+ * update. Averaging, the global-norm clip, the schedule, weight decay and the
+ * non-finite rule are gpt2_clip_adamw's. Per block weight W [rows, cols], with g
+ * the averaged and clipped gradient and m the array GPT2_ADAM_M:
+ *   m = momentum * m + g,   u = g + momentum * m,
+ *   W -= lr * (0.2 sqrt(max(rows, cols)) * NS5(u) + weight_decay * W),
+ * NS5 as gpt2op_orthogonalize with 5 steps; its factor gives the update the root
+ * mean square of AdamW's, so that one schedule serves both. GPT2_ADAM_V of those
+ * weights is left alone. 0 <= momentum < 1. workspace: device memory of at least
+ * gpt2_muon_workspace(cfg) bytes, 256-byte aligned. Not for the sharded step,
+ * whose shards cut through matrices. */
+size_t gpt2_muon_workspace(const gpt2_config* cfg);
+int gpt2_clip_muon(gpt2_model* model, int32_t step, float momentum, void* workspace, size_t ws_bytes,
+                   float* grad_norm_out);
 
 /* Total parameter count: real vocabulary rows only (124,439,808 for GPT-2
  * 124M, §4.1) when padded == 0, all stored rows when padded != 0. */

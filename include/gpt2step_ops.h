@@ -187,6 +187,65 @@ int gpt2op_lm_head_loss(const void* h, const void* wte, const int32_t* targets, 
 int gpt2op_softmax_ce_masked(void* logits, const int32_t* targets, float* losses, int N, int V, int Vp,
                              int ignore_index, float dscale, int* dev_err, void* stream);
 
+/* ---- post-training losses ---------------------------------------------------
+ * They reach the logits (bf16 [N,Vp], Vp % 8 == 0, 16-byte aligned) through each
+ * row's log-probability of its target over the V real ids,
+ *   lp = z[t] - log sum_{j<V} e^{z[j]},   dlp/dz[j] = [j = t] - p[j].
+ * A row whose target equals ignore_index is left out: its logits and its other
+ * inputs are not read, its outputs and gradient row are exactly 0. A target
+ * outside [0, V) does the same and sets flag 1. Columns >= V are not read into
+ * the softmax and get gradient 0. dlogits (bf16 [N,Vp]): NULL for no gradient,
+ * the logits themselves for a gradient in place, or memory that does not overlap
+ * them. Gradients are those of dscale * the sum of `losses`. */
+
+/* logps fp32 [N] = lp, 0 for rows left out. */
+int gpt2op_token_logps(const void* logits, const int32_t* targets, float* logps, int N, int V, int Vp, int ignore_index,
+                       int* dev_err, void* stream);
+
+/* Clipped policy loss with a KL term. With r = e^{lp - old_logp} and d = ref_logp - lp,
+ *   losses = weight * ( -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                       + kl_coef * (e^d - d - 1) )
+ *   dlosses/dlp = weight * ( -[r A <= clip(r) A] r A + kl_coef * (1 - e^d) ).
+ * An advantage A of 0 gives 0 for any r. old_logp, adv, weight (NULL: 1), ref_logp
+ * (NULL with kl_coef 0) fp32 [N]; logps (may be NULL) and losses fp32 [N].
+ * 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, all finite. */
+int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* old_logp, const float* ref_logp,
+                       const float* adv, const float* weight, void* dlogits, float* logps, float* losses, int N, int V,
+                       int Vp, int ignore_index, float clip_low, float clip_high, float kl_coef, float dscale,
+                       int* dev_err, void* stream);
+
+/* Paired preference loss. seq_start (device int32 [2P + 1], not decreasing, in
+ * [0, N]) cuts the rows into sequences; 2p is pair p's chosen sequence, 2p + 1 the
+ * rejected one. With S the sum of lp over a sequence's kept rows (with `average`
+ * divided by their number; 0 for none) and D = (S_c - ref_c) - (S_r - ref_r),
+ *   GPT2_PREFERENCE_SIGMOID  losses = -(1 - smoothing) log sigma(beta D) - smoothing log sigma(-beta D)
+ *   GPT2_PREFERENCE_SQUARED  losses = (D - 1 / (2 beta))^2          (smoothing 0)
+ * losses fp32 [P], seq_logps fp32 [2P] (may be NULL) = S, logps fp32 [N] = lp;
+ * ref_logp fp32 [2P] (NULL: 0). Rows in no sequence are left as they were, in
+ * logps and dlogits too. A pair with a bound that is not one gives loss 0, no
+ * gradient and flag 1. 0 < beta, 0 <= smoothing < 1. The workspace is 8-byte
+ * aligned; concurrent calls must not share one. */
+size_t gpt2op_preference_loss_workspace(int N, int P);
+int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int32_t* seq_start, const float* ref_logp,
+                           void* dlogits, float* logps, float* seq_logps, float* losses, int N, int P, int V, int Vp,
+                           int ignore_index, int kind, int average, float beta, float smoothing, float dscale,
+                           void* workspace, size_t ws_bytes, int* dev_err, void* stream);
+
+/* Newton-Schulz orthogonalisation, a batch of matrices [rows, cols] (x fp32 if
+ * x_fp32 else bf16, x_stride elements apart; out bf16, out_stride apart; rows and
+ * cols at most 16384, any alignment of the element type):
+ *   X = x / (|x|_F + 1e-7);   `steps` (1 .. 16) times   X = a X + (b G + c G G) X,  G = X X^T
+ * (for rows > cols from the other side, which is the same), (a, b, c) =
+ * (3.4445, -4.7750, 2.0315): the singular values go to about 0.7 .. 1.2, the
+ * singular vectors stay. Operands are fp16 with fp32 sums; five steps end about
+ * 1e-3 (relative, Frobenius) from the 64-bit result before the rounding of out.
+ * A zero matrix gives zeros; an infinity or NaN gives NaN in its own matrix.
+ * out must not overlap x. The workspace is 256-byte aligned; concurrent calls
+ * must not share one. */
+size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols);
+int gpt2op_orthogonalize(const void* x, int x_fp32, int64_t x_stride, void* out, int64_t out_stride, int batch,
+                         int rows, int cols, int steps, void* workspace, size_t ws_bytes, int* dev_err, void* stream);
+
 /* Token + position embedding: out[b,t,:] = wte[tok[b,t],:] + wpe[t,:] (bf16).
  * Ids outside [0, V) read row 0 and set flag 1 in dev_err. */
 int gpt2op_embedding_fwd(const int32_t* tokens, const void* wte, const void* wpe, void* out, int B, int T, int C,

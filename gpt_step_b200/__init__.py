@@ -195,10 +195,6 @@ def _kind(name: str) -> int:
     return PREFERENCE_KINDS[name]
 
 
-def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
-
-
 def _rows_of(T: int, tokens) -> int:
     n = tokens.numel()
     if n == 0 or n % T:
@@ -206,27 +202,44 @@ def _rows_of(T: int, tokens) -> int:
     return n
 
 
-def _want(dtype: str, numel, device=None, optional: bool = False, **tensors):
-    """Check device tensors against a type, an element count (None: any), contiguity and
-    a device (None: the first one's); returns the device."""
-    for name, t in tensors.items():
-        if t is None:
-            if optional:
-                continue
-            raise ValueError(f"{name} is required")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: a device tensor is needed")
-        if str(t.dtype) != "torch." + dtype:
-            raise ValueError(f"{name}: {t.dtype}, not {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: not contiguous")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{name}: {t.numel()} elements, not {numel}")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name}: on {t.device}, not {device}")
-    return device
+_dtypes = None
+
+
+def _types():
+    """(bfloat16, float32, int32, uint8), once torch is needed."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = (torch.bfloat16, torch.float32, torch.int32, torch.uint8)
+    return _dtypes
+
+
+def _device_of(t, name) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a device tensor is needed")
+    return dev
+
+
+def _need(t, name, dtype, numel, dev):
+    """Check a contiguous tensor's type, element count (-1: any but none) and device; returns its pointer."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    n = t.numel()
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (n == numel or (numel < 0 and n)):
+        return t.data_ptr()
+    _device_of(t, name)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    raise ValueError(f"{name}: {n} elements" + (f", not {numel}" if numel >= 0 else ""))
+
+
+def _opt(t, name, dtype, numel, dev):
+    return None if t is None else _need(t, name, dtype, numel, dev)
 
 
 @dataclass
@@ -278,43 +291,46 @@ class GPT2:
 
     def token_logps(self, tokens, targets, logps, ignore_index: int = -1):
         """logps (device fp32, tokens' shape) = the targets' log-probabilities, 0 where ignored."""
-        n = _rows_of(self.T, tokens)
-        dev = _want("int32", n, tokens=tokens, targets=targets)
-        _want("float32", n, dev, logps=logps)
-        check(lib().gpt2_token_logps(self.h, _ptr(tokens), _ptr(targets), n // self.T, ignore_index, _ptr(logps)),
-              "gpt2_token_logps")
+        _, f32, i32, _ = _types()
+        n, dev = _rows_of(self.T, tokens), self.arena.get_device()
+        check(lib().gpt2_token_logps(self.h, _need(tokens, "tokens", i32, n, dev), _need(targets, "targets", i32, n, dev),
+                                     n // self.T, ignore_index, _need(logps, "logps", f32, n, dev)), "gpt2_token_logps")
 
     def fwd_bwd_policy(self, tokens, targets, old_logp, adv, ref_logp=None, weight=None, ignore_index: int = -1,
                        clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0,
                        logps=None, want_loss: bool = False):
         """One micro-step on the clipped policy loss; per-position inputs are device fp32 [B, T]."""
-        n = self.B * self.T
-        dev = _want("int32", n, tokens=tokens, targets=targets)
-        _want("float32", n, dev, old_logp=old_logp, adv=adv)
-        _want("float32", n, dev, True, ref_logp=ref_logp, weight=weight, logps=logps)
+        _, f32, i32, _ = _types()
+        n, dev = self.B * self.T, self.arena.get_device()
         out = ctypes.c_float()
-        check(lib().gpt2_fwd_bwd_policy(self.h, _ptr(tokens), _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(adv),
-                                        _ptr(weight), ignore_index, clip_low, clip_high, kl_coef, scale, _ptr(logps),
-                                        ctypes.byref(out) if want_loss else None), "gpt2_fwd_bwd_policy")
+        check(lib().gpt2_fwd_bwd_policy(
+            self.h, _need(tokens, "tokens", i32, n, dev), _need(targets, "targets", i32, n, dev),
+            _need(old_logp, "old_logp", f32, n, dev), _opt(ref_logp, "ref_logp", f32, n, dev),
+            _need(adv, "adv", f32, n, dev), _opt(weight, "weight", f32, n, dev), ignore_index, clip_low, clip_high,
+            kl_coef, scale, _opt(logps, "logps", f32, n, dev), ctypes.byref(out) if want_loss else None),
+            "gpt2_fwd_bwd_policy")
         return out.value if want_loss else None
 
     def fwd_bwd_preference(self, tokens, targets, ref_logp=None, ignore_index: int = -1, kind: str = "sigmoid",
                            average: bool = False, beta: float = 0.1, smoothing: float = 0.0, seq_logps=None,
                            want_loss: bool = False):
         """One micro-step on the paired preference loss: sequences 2p (chosen) and 2p + 1 (rejected)."""
-        dev = _want("int32", self.B * self.T, tokens=tokens, targets=targets)
-        _want("float32", self.B, dev, True, ref_logp=ref_logp, seq_logps=seq_logps)
+        _, f32, i32, _ = _types()
+        n, dev = self.B * self.T, self.arena.get_device()
         out = ctypes.c_float()
-        check(lib().gpt2_fwd_bwd_preference(self.h, _ptr(tokens), _ptr(targets), _ptr(ref_logp), ignore_index,
-                                            _kind(kind), 1 if average else 0, beta, smoothing, _ptr(seq_logps),
-                                            ctypes.byref(out) if want_loss else None), "gpt2_fwd_bwd_preference")
+        check(lib().gpt2_fwd_bwd_preference(
+            self.h, _need(tokens, "tokens", i32, n, dev), _need(targets, "targets", i32, n, dev),
+            _opt(ref_logp, "ref_logp", f32, self.B, dev), ignore_index, _kind(kind), 1 if average else 0, beta,
+            smoothing, _opt(seq_logps, "seq_logps", f32, self.B, dev), ctypes.byref(out) if want_loss else None),
+            "gpt2_fwd_bwd_preference")
         return out.value if want_loss else None
 
     def clip_muon(self, step: int, workspace, momentum: float = 0.95, want_norm: bool = False):
         """The optimizer step with orthogonalised momentum for the blocks' 2-D weights;
         workspace: a device tensor of at least muon_workspace(cfg) bytes."""
         out = ctypes.c_float()
-        check(lib().gpt2_clip_muon(self.h, step, momentum, _ptr(workspace), _nbytes(workspace),
+        ws = _need(workspace, "workspace", _types()[3], -1, self.arena.get_device())
+        check(lib().gpt2_clip_muon(self.h, step, momentum, ws, workspace.numel(),
                                    ctypes.byref(out) if want_norm else None), "gpt2_clip_muon")
         return out.value if want_norm else None
 
@@ -609,26 +625,24 @@ def embedding_bwd(tokens, dx, dwte, dwpe, V, stream=None):
                                      _s(stream)), "gpt2op_embedding_bwd")
 
 
-# The post-training operators check their tensors, and run on the tensors' device.
+# The post-training operators check their tensors (the checks cost about as much as
+# the launch, which is what a call on few rows takes) and run on the tensors' device.
 
-class _on:
-    """The tensors' device as the current one, where it is not, and its stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"stream on {self.stream.device}, tensors on {device}")
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(name, dev, stream, *args):
+    """lib().<name>(*args, stream) with device `dev` current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = f(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, stream.cuda_stream)
+    if st:
+        raise GPT2Error(st, name)
 
 
 def _logits_shape(logits, V):
@@ -642,14 +656,11 @@ def _logits_shape(logits, V):
 
 def token_logps(logits, targets, logps, V, err, ignore_index=-1, stream=None):
     """logps = each row's log-probability of its target over the V real ids (0 where ignored)."""
+    b16, f32, i32, _ = _types()
     N, Vp = _logits_shape(logits, V)
-    dev = _want("bfloat16", None, logits=logits)
-    _want("int32", N, dev, targets=targets)
-    _want("int32", None, dev, err=err)
-    _want("float32", N, dev, logps=logps)
-    with _on(dev, stream) as s:
-        check(lib().gpt2op_token_logps(_ptr(logits), _ptr(targets), _ptr(logps), N, V, Vp, ignore_index, _ptr(err), s),
-              "gpt2op_token_logps")
+    d = _device_of(logits, "logits")
+    _call("gpt2op_token_logps", d, stream, _need(logits, "logits", b16, -1, d), _need(targets, "targets", i32, N, d),
+          _need(logps, "logps", f32, N, d), N, V, Vp, ignore_index, _need(err, "err", i32, -1, d))
 
 
 def policy_loss(logits, targets, old_logp, adv, dlogits, logps, losses, V, err, ref_logp=None, weight=None,
@@ -658,17 +669,14 @@ def policy_loss(logits, targets, old_logp, adv, dlogits, logps, losses, V, err, 
 
     dlogits: None (losses alone), the logits (in place) or a tensor of their shape;
     logps may be None; ref_logp is required with kl_coef > 0."""
+    b16, f32, i32, _ = _types()
     N, Vp = _logits_shape(logits, V)
-    dev = _want("bfloat16", None, logits=logits)
-    _want("bfloat16", N * Vp, dev, True, dlogits=dlogits)
-    _want("int32", N, dev, targets=targets)
-    _want("int32", None, dev, err=err)
-    _want("float32", N, dev, old_logp=old_logp, adv=adv, losses=losses)
-    _want("float32", N, dev, True, ref_logp=ref_logp, weight=weight, logps=logps)
-    with _on(dev, stream) as s:
-        check(lib().gpt2op_policy_loss(_ptr(logits), _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(adv),
-                                       _ptr(weight), _ptr(dlogits), _ptr(logps), _ptr(losses), N, V, Vp, ignore_index,
-                                       clip_low, clip_high, kl_coef, dscale, _ptr(err), s), "gpt2op_policy_loss")
+    d = _device_of(logits, "logits")
+    _call("gpt2op_policy_loss", d, stream, _need(logits, "logits", b16, -1, d), _need(targets, "targets", i32, N, d),
+          _need(old_logp, "old_logp", f32, N, d), _opt(ref_logp, "ref_logp", f32, N, d), _need(adv, "adv", f32, N, d),
+          _opt(weight, "weight", f32, N, d), _opt(dlogits, "dlogits", b16, N * Vp, d), _opt(logps, "logps", f32, N, d),
+          _need(losses, "losses", f32, N, d), N, V, Vp, ignore_index, clip_low, clip_high, kl_coef, dscale,
+          _need(err, "err", i32, -1, d))
 
 
 def preference_loss_workspace(N, P):
@@ -679,23 +687,18 @@ def preference_loss(logits, targets, seq_start, dlogits, logps, seq_logps, losse
                     ignore_index=-1, kind="sigmoid", average=False, beta=0.1, smoothing=0.0, dscale=1.0, stream=None):
     """Paired preference loss and its gradient over the logits; seq_start int32 [2P + 1],
     sequence 2p chosen and 2p + 1 rejected. dlogits as in policy_loss; seq_logps may be None."""
+    b16, f32, i32, u8 = _types()
     N, Vp = _logits_shape(logits, V)
     P = (seq_start.numel() - 1) // 2
     if P < 1 or seq_start.numel() != 2 * P + 1:
         raise ValueError(f"seq_start: {seq_start.numel()} bounds are not 2P + 1")
-    dev = _want("bfloat16", None, logits=logits)
-    _want("bfloat16", N * Vp, dev, True, dlogits=dlogits)
-    _want("int32", N, dev, targets=targets)
-    _want("int32", None, dev, seq_start=seq_start, err=err)
-    _want("float32", N, dev, logps=logps)
-    _want("float32", P, dev, losses=losses)
-    _want("float32", 2 * P, dev, True, ref_logp=ref_logp, seq_logps=seq_logps)
-    _want("uint8", None, dev, workspace=workspace)
-    with _on(dev, stream) as s:
-        check(lib().gpt2op_preference_loss(_ptr(logits), _ptr(targets), _ptr(seq_start), _ptr(ref_logp), _ptr(dlogits),
-                                           _ptr(logps), _ptr(seq_logps), _ptr(losses), N, P, V, Vp, ignore_index,
-                                           _kind(kind), 1 if average else 0, beta, smoothing, dscale, _ptr(workspace),
-                                           workspace.numel(), _ptr(err), s), "gpt2op_preference_loss")
+    d = _device_of(logits, "logits")
+    _call("gpt2op_preference_loss", d, stream, _need(logits, "logits", b16, -1, d),
+          _need(targets, "targets", i32, N, d), _need(seq_start, "seq_start", i32, -1, d),
+          _opt(ref_logp, "ref_logp", f32, 2 * P, d), _opt(dlogits, "dlogits", b16, N * Vp, d),
+          _need(logps, "logps", f32, N, d), _opt(seq_logps, "seq_logps", f32, 2 * P, d),
+          _need(losses, "losses", f32, P, d), N, P, V, Vp, ignore_index, _kind(kind), 1 if average else 0, beta,
+          smoothing, dscale, _need(workspace, "workspace", u8, -1, d), workspace.numel(), _need(err, "err", i32, -1, d))
 
 
 def orthogonalize_workspace(batch, rows, cols):
@@ -715,19 +718,17 @@ def _matrices(name, t):
 def orthogonalize(x, out, workspace, err, steps=5, stream=None):
     """out = the Newton-Schulz orthogonalisation of x: [rows, cols] or [batch, rows, cols]
     (matrices may lie apart), x fp32 or bf16, out bf16."""
+    b16, f32, i32, u8 = _types()
     b, r, c, xs = _matrices("x", x)
     ob, orows, oc, os_ = _matrices("out", out)
     if (ob, orows, oc) != (b, r, c):
         raise ValueError(f"out: {tuple(out.shape)}, x: {tuple(x.shape)}")
-    x_fp32 = str(x.dtype) == "torch.float32"
-    if not x_fp32 and str(x.dtype) != "torch.bfloat16":
+    if x.dtype is not f32 and x.dtype is not b16:
         raise ValueError(f"x: {x.dtype}, not float32 or bfloat16")
-    if str(out.dtype) != "torch.bfloat16":
+    if out.dtype is not b16:
         raise ValueError(f"out: {out.dtype}, not bfloat16")
-    if not x.is_cuda or out.device != x.device:
-        raise ValueError(f"x on {x.device}, out on {out.device}: one GPU is needed")
-    _want("uint8", None, x.device, workspace=workspace)
-    _want("int32", None, x.device, err=err)
-    with _on(x.device, stream) as s:
-        check(lib().gpt2op_orthogonalize(_ptr(x), 1 if x_fp32 else 0, xs, _ptr(out), os_, b, r, c, steps,
-                                         _ptr(workspace), workspace.numel(), _ptr(err), s), "gpt2op_orthogonalize")
+    d = _device_of(x, "x")
+    if out.get_device() != d:
+        raise ValueError(f"out: on {out.device}, not cuda:{d}")
+    _call("gpt2op_orthogonalize", d, stream, x.data_ptr(), 1 if x.dtype is f32 else 0, xs, out.data_ptr(), os_, b, r, c,
+          steps, _need(workspace, "workspace", u8, -1, d), workspace.numel(), _need(err, "err", i32, -1, d))

@@ -555,14 +555,15 @@ int spec_loss(gpt2_model* m, const LossSpec& spec, const int32_t* tgt, int N, bf
     a.targets = tgt; a.logps = spec.logps; a.losses = losses;
     a.part = lse_part; a.slots = slots; a.V = d.V; a.Vp = d.Vp; a.ignore_index = spec.ignore_index;
     a.err = m->err();
-    GPT2_TRY(pt::policy_loss(a, N, s));
+    a.N = N;
+    GPT2_TRY(pt::policy_loss(a, s));
     n_loss = N;
     factor = a.dscale;
   } else {
     pt::RowArgs r{};
     r.logits = tgt_val ? nullptr : logits;
     r.targets = tgt; r.part = lse_part; r.tgt_val = tgt_val; r.slots = slots; r.V = d.V; r.Vp = d.Vp;
-    r.ignore_index = spec.ignore_index; r.err = m->err();
+    r.ignore_index = spec.ignore_index; r.err = m->err(); r.N = N;
     r.logps = spec.kind == LossSpec::LOGPS ? spec.logps : losses;
     // the row and pair scratch lives in the attention backward's per-query terms,
     // which are free until that runs (32 bytes a row and head)
@@ -570,17 +571,17 @@ int spec_loss(gpt2_model* m, const LossSpec& spec, const int32_t* tgt, int N, bf
     float2* stats = m->at<float2>(y.attD);
     float* coef = reinterpret_cast<float*>(stats + d.N);
     if (spec.kind == LossSpec::PREFERENCE) r.stats = stats;
-    GPT2_TRY(pt::row_logps(r, N, s));
+    GPT2_TRY(pt::row_logps(r, s));
     if (spec.kind == LossSpec::PREFERENCE) {
       pt::PairArgs a = spec.pair;
       a.logps = losses; a.targets = tgt; a.seq_start = nullptr; a.seq_len = d.T; a.N = N; a.V = d.V;
       a.ignore_index = spec.ignore_index; a.coef = coef; a.losses = coef + 2 * P; a.err = m->err();
-      launch_pdl(pt::pair_kernel, dim3(P), dim3(pt::kRowThreads), 0, s, a);
+      GPT2_TRY(pt::pair_losses(a, P, s));
       pt::PairGradArgs g{};
       g.logits = g.dlogits = logits;
       g.targets = tgt; g.stats = stats; g.coef = coef; g.n_seq = 2 * P; g.seq_len = d.T; g.V = d.V; g.Vp = d.Vp;
-      g.ignore_index = spec.ignore_index;
-      launch_pdl(pt::pair_grad_kernel, dim3(N), dim3(pt::kRowThreads), 0, s, g);
+      g.ignore_index = spec.ignore_index; g.N = N;
+      GPT2_TRY(pt::pair_gradients(g, s));
       nl += 2;
       n_loss = P;
       loss_src = a.losses;
@@ -1658,8 +1659,9 @@ int gpt2op_token_logps(const void* logits, const int32_t* targets, float* logps,
   if (!logits || !targets || !logps || !dev_err || !pt::logits_ok(logits, N, V, Vp)) return GPT2_ERR_ARG;
   pt::RowArgs r{};
   r.logits = static_cast<const bf16*>(logits);
-  r.targets = targets; r.logps = logps; r.V = V; r.Vp = Vp; r.ignore_index = ignore_index; r.err = dev_err;
-  return pt::row_logps(r, N, static_cast<cudaStream_t>(stream));
+  r.targets = targets; r.logps = logps; r.N = N; r.V = V; r.Vp = Vp; r.ignore_index = ignore_index;
+  r.err = dev_err;
+  return pt::row_logps(r, static_cast<cudaStream_t>(stream));
 }
 
 int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* old_logp, const float* ref_logp,
@@ -1674,7 +1676,8 @@ int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* 
   a.targets = targets; a.old_logp = old_logp; a.adv = adv; a.weight = weight;
   a.dlogits = static_cast<bf16*>(dlogits);
   a.logps = logps; a.losses = losses; a.V = V; a.Vp = Vp; a.ignore_index = ignore_index; a.err = dev_err;
-  return pt::policy_loss(a, N, static_cast<cudaStream_t>(stream));
+  a.N = N;
+  return pt::policy_loss(a, static_cast<cudaStream_t>(stream));
 }
 
 size_t gpt2op_preference_loss_workspace(int N, int P) { return N > 0 && P > 0 ? pt::preference_workspace(N, P) : 0; }
@@ -1694,20 +1697,21 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
   pt::RowArgs r{};
   r.logits = static_cast<const bf16*>(logits);
   r.targets = targets; r.logps = logps; r.stats = stats; r.seq_start = seq_start; r.n_seq = 2 * P; r.V = V; r.Vp = Vp;
-  r.ignore_index = ignore_index; r.err = dev_err;
-  GPT2_TRY(pt::row_logps(r, N, s));
+  r.ignore_index = ignore_index; r.err = dev_err; r.N = N;
+  GPT2_TRY(pt::row_logps(r, s));
   a.logps = logps; a.targets = targets; a.seq_start = seq_start; a.ref_logp = ref_logp; a.seq_logps = seq_logps;
   a.losses = losses; a.coef = reinterpret_cast<float*>(stats + N); a.N = N; a.V = V; a.ignore_index = ignore_index;
   a.err = dev_err;
-  launch_pdl(pt::pair_kernel, dim3(P), dim3(pt::kRowThreads), 0, s, a);
+  GPT2_TRY(pt::pair_losses(a, P, s));
   if (dlogits) {
     pt::PairGradArgs g{};
     g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats; g.coef = a.coef;
     g.dlogits = static_cast<bf16*>(dlogits);
     g.n_seq = 2 * P; g.V = V; g.Vp = Vp; g.ignore_index = ignore_index;
-    launch_pdl(pt::pair_grad_kernel, dim3(N), dim3(pt::kRowThreads), 0, s, g);
+    g.N = N;
+    return pt::pair_gradients(g, s);
   }
-  return cudaGetLastError() == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
+  return GPT2_OK;
 }
 
 size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols) {

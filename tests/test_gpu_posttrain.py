@@ -59,7 +59,8 @@ def policy_inputs(rng, z, t, V):
 
 
 SIZES = [(1, 1, 8), (3, 2, 8), (5, 9, 16), (64, 1000, 1024), (37, 1000, 1000), (33, 4353, 4480), (7, 8449, 8576),
-         (130, 2040, 2048), (9, 50257, 50304), (5, 30011, 30016), (4, 120001, 120008)]
+         (130, 2040, 2048), (9, 50257, 50304), (5, 30011, 30016), (700, 33001, 33008), (4, 90003, 90008),
+         (4, 120001, 120008)]
 
 
 def scale_of(lp, old, ref, adv, w, kl, ds):
@@ -118,8 +119,8 @@ def test_policy_loss_alone_and_bad_targets():
     assert np.all((np.abs(host(dz) - rdz) <= tol)[rest])
 
 
-def test_rows_without_a_finite_log_probability_stay_in_their_rows():
-    V, Vp = 40, 48
+@pytest.mark.parametrize("V,Vp", [(40, 48), (5000, 5008), (40001, 40008)])
+def test_rows_without_a_finite_log_probability_stay_in_their_rows(V, Vp):
     z = np.zeros((5, Vp))
     z[0, 3] = np.nan
     z[1, :V] = -np.inf
@@ -136,6 +137,32 @@ def test_rows_without_a_finite_log_probability_stay_in_their_rows():
     assert abs(lp[2] + math.log(V - 1)) < 1e-6 and abs(lp[4] + math.log(V)) < 1e-6
     assert ls[3] == 0 and np.all(d[3] == 0) and d[2, 7] == 0
     assert np.all(np.isfinite(d[[2, 4]])) and np.all(d[:, V:] == 0)
+
+
+@pytest.mark.parametrize("V,Vp", [(1000, 1024), (9000, 9000), (40001, 40008), (120001, 120008)])
+def test_targets_far_below_the_largest_logit(V, Vp):
+    """Differences past the exponents of fp32, both ways: log-probabilities and gradients stay finite."""
+    rng = np.random.default_rng(V)
+    z = rounded(rng.standard_normal((6, Vp)))
+    t = np.array([3, 5, 7, V - 1, 11, 13])
+    z[0, 4] = z[1, 6] = 400.0                              # the target 400 below another id
+    z[2, 7] = 400.0                                        # and above all
+    z[3, :V] -= 30000.0
+    z[4, :V] += 30000.0
+    old = np.zeros(6)
+    z = rounded(z)
+    lp, p, keep = PT.token_logps(z, t, V)
+    old = np.where(lp < -80, lp, 0.0)
+    rl, rlp, rdz = PT.policy_loss(z, t, V, old.astype(np.float32), np.ones(6), clip_high=0.5)
+    losses, logps, err = torch.empty(6, device="cuda"), torch.empty(6, device="cuda"), err_word()
+    dz = torch.empty(6, Vp, dtype=torch.bfloat16, device="cuda")
+    gs.policy_loss(bf16(z), i32(t), f32(old), f32(np.ones(6)), dz, logps, losses, V, err, clip_high=0.5)
+    # the logits themselves are large here: y - c is one rounding of a difference, its factor log2(e) 2^-25
+    tol = 2.0 ** -19 + 2.0 ** -22 * np.abs(rlp)
+    assert np.all(np.abs(host(logps) - rlp) <= tol)
+    g = np.abs(np.exp(np.minimum(rlp - old, 1.0)))
+    assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g) + (tol * g)[:, None])
+    assert int(err.sum()) == 0
 
 
 def ragged(rng, S, most, gap=True):

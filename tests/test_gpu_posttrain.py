@@ -283,7 +283,8 @@ def run_ns(x, steps=5, **kw):
 
 @pytest.mark.parametrize("r,c", [(1, 1), (1, 7), (9, 1), (5, 7), (16, 16), (64, 64), (63, 65), (65, 64), (128, 128),
                                  (129, 127), (130, 257), (300, 200), (257, 1000), (384, 384), (640, 200), (100, 2100),
-                                 (513, 770)])
+                                 (513, 770), (100, 140), (128, 256), (77, 333), (520, 96), (1000, 128), (1500, 33),
+                                 (128, 2048), (2048, 100), (17, 2049)])
 @pytest.mark.parametrize("fp32", [True, False])
 def test_orthogonalize(r, c, fp32):
     rng = np.random.default_rng(r * 10000 + c)
@@ -294,6 +295,8 @@ def test_orthogonalize(r, c, fp32):
     for g, q in zip(got, ref):
         assert rel_l2(g, q) <= ns_tol(r, c)
     assert np.array_equal(run_ns(xd[1]), got[1])           # a matrix alone, the same bits
+    many = xd.repeat(20, 1, 1) if r * c < 300000 else xd    # more matrices than fit at a time
+    assert np.array_equal(run_ns(many)[-3:], got)
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 8])

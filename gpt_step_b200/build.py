@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgpt2step.so")
 SOURCES = ["gpt2step.cu"]
 DEPS = ["common.cuh", "gemm.cuh", "gemm2sm.cuh", "attention.cuh", "attention_tc.cuh", "kernels.cuh",
-        "muon.cuh", "muon_small.cuh", "posttrain.cuh"]
+        "muon.cuh", "muon_pair.cuh", "muon_small.cuh", "muon_step.cuh", "posttrain.cuh"]
 HEADERS = [os.path.join(ROOT, "include", h) for h in ("gpt2step.h", "gpt2step_ops.h")]
 
 NVCC_FLAGS = [

@@ -30,8 +30,7 @@
 #include "gemm.cuh"
 #include "gemm2sm.cuh"
 #include "kernels.cuh"
-#include "muon.cuh"
-#include "muon_small.cuh"
+#include "muon_step.cuh"
 #include "posttrain.cuh"
 
 namespace {
@@ -1727,14 +1726,6 @@ int gpt2op_orthogonalize(const void* x, int x_fp32, int64_t x_stride, void* out,
   if (batch > 1 && (x_stride < (int64_t)rows * cols || out_stride < (int64_t)rows * cols)) return GPT2_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bf16* o = static_cast<bf16*>(out);
-  if (ws_bytes < gpt2op_orthogonalize_workspace(batch, rows, cols) || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
-      gpt2op_orthogonalize_workspace(batch, rows, cols) == 0 || steps < 1 || steps > muon::kMaxSteps)
-    return GPT2_ERR_ARG;
-  if (muon::small::fits(std::min(rows, cols), std::max(rows, cols)))
-    return x_fp32 ? muon::small::run(static_cast<const float*>(x), x_stride, o, out_stride, batch, rows, cols, steps,
-                                     dev_err, s)
-                  : muon::small::run(static_cast<const bf16*>(x), x_stride, o, out_stride, batch, rows, cols, steps,
-                                     dev_err, s);
   return x_fp32 ? muon::orthogonalize(static_cast<const float*>(x), x_stride, o, out_stride, batch, rows, cols, steps,
                                       workspace, ws_bytes, dev_err, s)
                 : muon::orthogonalize(static_cast<const bf16*>(x), x_stride, o, out_stride, batch, rows, cols, steps,

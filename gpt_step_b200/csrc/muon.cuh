@@ -73,264 +73,121 @@ __global__ void __launch_bounds__(256) ns_sumsq_kernel(const T* __restrict__ x, 
 }
 
 // ---------------------------------------------------------------------------
-// X = M / (|M|_F + 1e-7), times 2^10, as hi and lo [batch][n][ld] fp16;
-// 64 x 64 tiles through shared memory, transposed for tall matrices
+// X = M / (|M|_F + 1e-7), times 2^10, as hi and lo [batch][n][ld] fp16, its padding 0;
+// and the counters of the rounds at 0. A thread forms 8 columns of a row; tall matrices
+// come through shared memory, 64 x 64 at a time.
 // ---------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(256) ns_convert_kernel(const T* __restrict__ x, long stride, int rows, int cols,
-                                                         const double* __restrict__ part, int parts,
-                                                         __half* __restrict__ hi, __half* __restrict__ lo, int ld) {
-  pdl_begin();
-  __shared__ float tile[64][65];
-  __shared__ float mul;
-  if (threadIdx.x < 32) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += 32) s += part[(size_t)blockIdx.z * parts + i];
-    s = warp_sum_d(s);
-    if (threadIdx.x == 0) mul = (float)((double)kScale / (sqrt(s) + 1e-7));
-  }
-  const bool tall = rows > cols;
-  const int n = tall ? cols : rows, m = tall ? rows : cols;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of X
-  const T* src = x + (size_t)blockIdx.z * stride;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int i = ty; i < 64; i += 4) {
-    // the inner index runs along the stored rows of M either way
-    const int xr = tall ? r0 + tx : r0 + i, xc = tall ? c0 + i : c0 + tx;
-    float v = 0.f;
-    if (xr < n && xc < m) v = load1(src + (tall ? (size_t)xc * cols + xr : (size_t)xr * cols + xc));
-    if (tall) tile[tx][i] = v;
-    else tile[i][tx] = v;
-  }
-  __syncthreads();
-  const float mu = mul;
-  for (int i = ty; i < 64; i += 4) {
-    const int xr = r0 + i, xc = c0 + tx;
-    if (xr >= n || xc >= ld) continue;
-    const float v = tile[i][tx] * mu;
-    const __half h = __float2half_rn(v);
-    const size_t at = ((size_t)blockIdx.z * n + xr) * ld + xc;
-    hi[at] = h;
-    lo[at] = __float2half_rn(v - __half2float(h));
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the three products
-// ---------------------------------------------------------------------------
-enum Mode : int { GRAM = 0, POLY = 1, APPLY = 2, LAST = 3 };
-
-constexpr int BM = 128, BN = 128, BK = 64, STAGES = 3;
-constexpr int kStageBytes = (BM + BN) * BK * 2;
-constexpr int kSmem = STAGES * kStageBytes + 1024 + 256;
-constexpr int kThreads = 192;
-
-struct Params {
-  int n, m, ld_x, ld_a;      // X is [n][m], its rows ld_x apart; A, Q are [n][n], rows ld_a apart
-  int nkb;                   // 64-wide blocks of the reduction
-  __half* out;               // GRAM: A, POLY: Q, APPLY: the next X's hi
-  const __half* aux;         // POLY: A, APPLY and LAST: X's hi
-  __half* lo;                // APPLY: X's lo, read (use_lo) and written (put_lo); LAST: read
-  bf16* result;              // LAST: [rows][cols], transposed back for tall matrices
-  long result_stride;
-  int rows, cols;
-  int use_lo, put_lo;
-  int* err;
-};
-
-GPT2_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-// fp16 x fp16 -> fp32
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 GPT2_DEV uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-GPT2_DEV void load_half32(const __half* p, float (&v)[32]) {
+// hi and lo of eight values
+GPT2_DEV void split8(const float* f, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * j);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-      v[8 * j + 2 * h] = f.x;
-      v[8 * j + 2 * h + 1] = f.y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    l[i] = pack_half2(f[2 * i] - v.x, f[2 * i + 1] - v.y);
   }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-GPT2_DEV void store_half32(__half* p, const float (&v)[32]) {
+// Eight neighbouring elements, in 16-byte loads if `vec`; those from `valid` on are 0.
+template <typename T>
+GPT2_DEV void load8(const T* p, int valid, bool vec, float (&f)[8]) {
+  if (vec && valid >= 8) {
+    constexpr int E = 16 / sizeof(T);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(p + 8 * j) =
-        make_uint4(pack_half2(v[8 * j], v[8 * j + 1]), pack_half2(v[8 * j + 2], v[8 * j + 3]),
-                   pack_half2(v[8 * j + 4], v[8 * j + 5]), pack_half2(v[8 * j + 6], v[8 * j + 7]));
-}
-
-// One 128 x 128 output tile a CTA: warp 0 brings operands in by TMA, warp 1
-// issues the MMAs, warps 2..5 run the epilogue. A and Q are symmetric: their
-// tiles below the diagonal are computed and written to both places.
-template <int MODE>
-__global__ void __launch_bounds__(kThreads, 2)
-    ns_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const Params p) {
-  extern __shared__ __align__(1024) uint8_t ns_smem[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ns_smem) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * kStageBytes);
-  uint64_t* empty = full + STAGES;
-  uint64_t* done = empty + STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  constexpr bool SYM = MODE == GRAM || MODE == POLY;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1);
+    for (int q = 0; q < 8; q += E) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + q));
+      const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[q + j] = load1(e + j);
     }
-    mbar_init(smem_u32(done), 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), BN);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pdl_begin();
-
-  int ti, tj;
-  if (SYM) {
-    // tile index -> (ti, tj), tj <= ti
-    ti = (int)((sqrtf(8.f * blockIdx.x + 1.f) - 1.f) * 0.5f);
-    while ((ti + 1) * (ti + 2) / 2 <= (int)blockIdx.x) ++ti;
-    while (ti * (ti + 1) / 2 > (int)blockIdx.x) --ti;
-    tj = blockIdx.x - ti * (ti + 1) / 2;
   } else {
-    const int num_m = (p.n + BM - 1) / BM;
-    ti = blockIdx.x % num_m;
-    tj = blockIdx.x / num_m;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] = q < valid ? load1(p + q) : 0.f;
   }
+}
+
+template <typename T, bool TALL>
+__global__ void __launch_bounds__(256) ns_convert_kernel(const T* __restrict__ x, long stride, int rows, int cols,
+                                                         const double* __restrict__ part, int parts,
+                                                         __half* __restrict__ hi, __half* __restrict__ lo, int ld,
+                                                         int vec, uint32_t* __restrict__ count) {
+  pdl_begin();
+  __shared__ float tile[TALL ? 64 : 1][65];
+  __shared__ float mul_s;
   const int z = blockIdx.y;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err)) break;
-        const uint32_t fb = smem_u32(&full[stage]);
-        mbar_arrive_expect_tx(fb, kStageBytes);
-        const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + BM * BK * 2;
-        tma_load_3d(sa, &tm_a, fb, kb * BK, ti * BM, z);
-        if (SYM) {
-          tma_load_3d(sb, &tm_b, fb, kb * BK, tj * BN, z);
-        } else {
-          for (int j = 0; j < BN / 64; ++j) tma_load_3d(sb + j * 8192, &tm_b, fb, tj * BN + 64 * j, kb * BK, z);
-        }
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(BM, BN, !SYM);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        if (!mbar_wait(smem_u32(&full[stage]), phase, p.err)) break;
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + BM * BK * 2;
-#pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t ad = smem_desc_sw128(sa + kk * 32, 16, 1024);
-          const uint64_t bd = SYM ? smem_desc_sw128(sb + kk * 32, 16, 1024)
-                                  : smem_desc_sw128(sb + kk * 2048, 8192, 1024);
-          tc_mma_bf16(tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-        }
-        tc_commit(smem_u32(&empty[stage]));
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
-      }
-      tc_commit(smem_u32(done));
-      mbar_wait(smem_u32(done), 0, p.err);
-    }
-  } else if (mbar_wait(smem_u32(done), 0, p.err)) {
-    tc_fence_after();
-    const int q = warp & 3;
-    const int row = ti * BM + q * 32 + lane;
-    const bool row_ok = row < p.n;
-    const int ld = SYM ? p.ld_a : p.ld_x;
-    const size_t zrow = ((size_t)z * p.n + row) * ld;
-#pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
-      const int col = tj * BN + c;
-      if (col >= ld) break;                 // ld is a multiple of 64
-      float v[32];
-      tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= MODE == POLY ? kC * kInvScale : kInvScale;
-      if (MODE != GRAM && row_ok) {
-        constexpr float f = MODE == POLY ? kB : kA;
-        float x[32];
-        load_half32(p.aux + zrow + col, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(f, x[i], v[i]);
-        if (MODE >= APPLY && p.use_lo) {
-          load_half32(p.lo + zrow + col, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(f, x[i], v[i]);
-        }
-      }
-      if (MODE == LAST) {
-        const bool tall = p.rows > p.cols;
-        bf16* res = p.result + (size_t)z * p.result_stride;
-        if (row_ok) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < p.m)
-              res[tall ? (size_t)(col + i) * p.cols + row : (size_t)row * p.cols + col + i] =
-                  __float2bfloat16_rn(v[i] * kInvScale);
-        }
-        continue;
-      }
-      if (row_ok) {
-        store_half32(p.out + zrow + col, v);
-        if (MODE == APPLY && p.put_lo) {
-          float l[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) l[i] = v[i] - __half2float(__float2half_rn(v[i]));
-          store_half32(p.lo + zrow + col, l);
-        }
-      }
-      if (SYM && ti != tj && row < ld) {
-        // the mirror image; rows n .. ld - 1 are 0 and become its padding
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col + i < p.n) p.out[((size_t)z * p.n + col + i) * ld + row] = __float2half_rn(v[i]);
-      }
-    }
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 32) s += part[(size_t)z * parts + i];
+    s = warp_sum_d(s);
+    if (threadIdx.x == 0) mul_s = (float)((double)kScale / (sqrt(s) + 1e-7));
+    if (blockIdx.x == 0 && threadIdx.x < 3) count[z * 3 + threadIdx.x] = 0;
   }
-
-  tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, BN);
+  const float mul = mul_s;
+  const int n = TALL ? cols : rows, m = TALL ? rows : cols;
+  const T* src = x + (size_t)z * stride;
+  auto put = [&](int r, int c, float (&f)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] *= mul;
+    uint4 h, l;
+    split8(f, h, l);
+    const size_t at = ((size_t)z * n + r) * ld + c;
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
+  };
+  if (!TALL) {
+    const int per_row = ld / 8;
+    const long units = (long)n * per_row;
+#pragma unroll 4
+    for (long u = blockIdx.x * 256L + threadIdx.x; u < units; u += gridDim.x * 256L) {
+      const int r = (int)(u / per_row), c = (int)(u - (long)r * per_row) * 8;
+      float f[8];
+      load8(src + (size_t)r * cols + c, m - c, vec, f);
+      put(r, c, f);
+    }
+  } else {
+    // tiles of 64 columns of X (rows of M) x 64 rows of X
+    const int tr = (n + 63) / 64;
+    const long tiles = (long)tr * (ld / 64);
+    for (long t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int r0 = (int)(t % tr) * 64, c0 = (int)(t / tr) * 64;
+      // 8 threads a row of M, 32 rows at a time
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = threadIdx.x / 8 + 32 * h, r = (threadIdx.x % 8) * 8;
+        float f[8];
+        load8(src + (size_t)(c0 + c) * cols + r0 + r, c0 + c < m ? n - r0 - r : 0, vec, f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) tile[c][r + q] = f[q];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = threadIdx.x / 8 + 32 * h, c = (threadIdx.x % 8) * 8;
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = tile[c + q][r];
+        if (r0 + r < n) put(r0 + r, c0 + c, f);
+      }
+      __syncthreads();
+    }
   }
+}
+
+// ---------------------------------------------------------------------------
+// shared by the kernels of the rounds
+// ---------------------------------------------------------------------------
+constexpr int BK = 64;   // fp16 elements of a 128-byte swizzle row
+
+// fp16 x fp16 -> fp32
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // ---------------------------------------------------------------------------
@@ -338,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------------------
 struct Work {
   int n, m, ld_x, ld_a, parts;
-  size_t x0, x1, lo, a, q, part, total;
+  size_t x0, x1, lo, a, q, part, count, total;
 };
 
 inline bool plan(int batch, int rows, int cols, Work* w) {
@@ -358,181 +215,31 @@ inline bool plan(int batch, int rows, int cols, Work* w) {
   w->a = take(ab);
   w->q = take(ab);
   w->part = take((size_t)batch * w->parts * 8);
+  w->count = take((size_t)batch * 3 * 4);
   w->total = o;
   return true;
 }
 
-// [batch][rows][ld] fp16; boxes of 64 columns x box_rows rows of one matrix
-inline bool map_3d(CUtensorMap* m, const __half* base, int ld, int rows, int batch, uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)ld, (cuuint64_t)rows, (cuuint64_t)batch};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * rows * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int MODE>
-cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int tiles, int batch,
-                        cudaStream_t s) {
-  static PerDeviceOnce once;
-  const cudaError_t e = smem_optin(once, ns_gemm_kernel<MODE>, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(ns_gemm_kernel<MODE>, dim3(tiles, batch), dim3(kThreads), kSmem, s, a, b, p);
-}
-
-// out[b] = the orthogonalised x[b], bf16 [rows][cols]; matrices x_stride, out_stride
-// elements apart. have_parts: the workspace holds the partial sums of squares already.
+// X of the batch into the workspace. have_parts: it holds the partial sums of squares already.
 template <typename T>
-int orthogonalize(const T* x, long x_stride, bf16* out, long out_stride, int batch, int rows, int cols, int steps,
-                  void* ws, size_t ws_bytes, int* err, cudaStream_t s, bool have_parts = false) {
-  Work w;
-  if (!plan(batch, rows, cols, &w) || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255))
-    return GPT2_ERR_ARG;
-  if (steps < 1 || steps > kMaxSteps) return GPT2_ERR_ARG;
-  char* base = static_cast<char*>(ws);
-  __half* xh[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
-  __half* lo = reinterpret_cast<__half*>(base + w.lo);
-  __half* a = reinterpret_cast<__half*>(base + w.a);
-  __half* q = reinterpret_cast<__half*>(base + w.q);
+cudaError_t prepare_x(const Work& w, char* base, const T* x, long x_stride, int batch, int rows, int cols,
+                      bool have_parts, cudaStream_t s) {
   double* part = reinterpret_cast<double*>(base + w.part);
-
-  CUtensorMap mx_rows[2], mx_cols[2], ma, mq;
-  for (int i = 0; i < 2; ++i)
-    if (!map_3d(&mx_rows[i], xh[i], w.ld_x, w.n, batch, BM) || !map_3d(&mx_cols[i], xh[i], w.ld_x, w.n, batch, 64))
-      return GPT2_ERR_CUDA;
-  if (!map_3d(&ma, a, w.ld_a, w.n, batch, BM) || !map_3d(&mq, q, w.ld_a, w.n, batch, BM)) return GPT2_ERR_CUDA;
-
-  const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (x_stride * sizeof(T)) % 16 == 0;
-  cudaError_t e = cudaSuccess;
-  if (!have_parts)
-    e = launch_pdl(ns_sumsq_kernel<T>, dim3(w.parts, batch), dim3(256), 0, s, x, x_stride, (long)rows * cols, vec, part);
-  if (e == cudaSuccess)
-    e = launch_pdl(ns_convert_kernel<T>, dim3(w.ld_x / 64, (w.n + 63) / 64, batch), dim3(256), 0, s, x, x_stride, rows,
-                   cols, (const double*)part, w.parts, xh[0], lo, w.ld_x);
-  const int nt = (w.n + BM - 1) / BM, mt = (w.m + BN - 1) / BN;
-  Params p{};
-  p.n = w.n; p.m = w.m; p.ld_x = w.ld_x; p.ld_a = w.ld_a;
-  p.rows = rows; p.cols = cols; p.err = err;
-  for (int i = 0; i < steps && e == cudaSuccess; ++i) {
-    const int cur = i & 1;
-    p.nkb = w.ld_x / 64;
-    p.out = a;
-    e = launch_gemm<GRAM>(mx_rows[cur], mx_rows[cur], p, nt * (nt + 1) / 2, batch, s);
-    if (e != cudaSuccess) break;
-    p.nkb = w.ld_a / 64;
-    p.out = q; p.aux = a;
-    e = launch_gemm<POLY>(ma, ma, p, nt * (nt + 1) / 2, batch, s);
-    if (e != cudaSuccess) break;
-    p.aux = xh[cur]; p.lo = lo;
-    p.use_lo = i < steps - 2; p.put_lo = i + 1 < steps - 2;
-    p.out = xh[cur ^ 1];
-    p.result = out; p.result_stride = out_stride;
-    e = i + 1 < steps ? launch_gemm<APPLY>(mq, mx_cols[cur], p, nt * mt, batch, s)
-                      : launch_gemm<LAST>(mq, mx_cols[cur], p, nt * mt, batch, s);
+  const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (batch == 1 || (x_stride * sizeof(T)) % 16 == 0);
+  if (!have_parts) {
+    const cudaError_t e = launch_pdl(ns_sumsq_kernel<T>, dim3(w.parts, batch), dim3(256), 0, s, x, x_stride,
+                                     (long)rows * cols, vec, part);
+    if (e != cudaSuccess) return e;
   }
-  return e == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
-}
-
-// ---------------------------------------------------------------------------
-// the optimizer's elementwise passes
-// ---------------------------------------------------------------------------
-// Momentum: mom = mu mom + g', u = g' + mu mom with g' = g * gscale; u takes the
-// gradient's place and its sum of squares goes to part[matrix][block]. A step
-// flagged non-finite leaves mom alone.
-__global__ void __launch_bounds__(256) momentum_kernel(float* __restrict__ g, float* __restrict__ mom, long stride,
-                                                       long count4, float mu, const float* __restrict__ gscale,
-                                                       const int* __restrict__ skip, double* __restrict__ part) {
-  pdl_begin();
-  __shared__ double red[8];
-  const float gs = *gscale;
-  const bool off = *skip != 0;
-  float4* g4 = reinterpret_cast<float4*>(g + (size_t)blockIdx.y * stride);
-  float4* m4 = reinterpret_cast<float4*>(mom + (size_t)blockIdx.y * stride);
-  double s = 0.0;
-  if (!off)
-    for (long i = blockIdx.x * 256L + threadIdx.x; i < count4; i += (long)gridDim.x * 256) {
-      float4 gv = g4[i], mv = m4[i];
-      float* gp = &gv.x;
-      float* mp = &mv.x;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float gg = gp[j] * gs;
-        mp[j] = mu * mp[j] + gg;
-        gp[j] = gg + mu * mp[j];
-        s += (double)gp[j] * gp[j];
-      }
-      m4[i] = mv;
-      g4[i] = gv;
-    }
-  s = warp_sum_d(s);
-  if (lane_id() == 0) red[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) s += red[w];
-    part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
-  }
-}
-
-// w -= lr (adj o + wd w), the bf16 copy, and g = 0; a flagged step only clears g.
-__global__ void __launch_bounds__(256) apply_kernel(float* __restrict__ w, bf16* __restrict__ wb, float* __restrict__ g,
-                                                    const bf16* __restrict__ o, long stride, long count4, float lr,
-                                                    float adj, float wd, const int* __restrict__ skip) {
-  pdl_begin();
-  const bool off = *skip != 0;
-  const size_t base = (size_t)blockIdx.y * stride;
-  float4* g4 = reinterpret_cast<float4*>(g + base);
-  float4* w4 = reinterpret_cast<float4*>(w + base);
-  uint2* b4 = reinterpret_cast<uint2*>(wb + base);
-  const uint2* o4 = reinterpret_cast<const uint2*>(o) + (size_t)blockIdx.y * count4;
-  for (long i = blockIdx.x * 256L + threadIdx.x; i < count4; i += (long)gridDim.x * 256) {
-    g4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (off) continue;
-    const uint2 ov = o4[i];
-    float4 wv = w4[i];
-    const float2 lo = unpack_bf16x2(ov.x), hi = unpack_bf16x2(ov.y);
-    wv.x -= lr * (adj * lo.x + wd * wv.x);
-    wv.y -= lr * (adj * lo.y + wd * wv.y);
-    wv.z -= lr * (adj * hi.x + wd * wv.z);
-    wv.w -= lr * (adj * hi.y + wd * wv.w);
-    w4[i] = wv;
-    b4[i] = make_uint2(pack_bf16x2(wv.x, wv.y), pack_bf16x2(wv.z, wv.w));
-  }
-}
-
-constexpr int kUpdateLaunches = 3 + 3 * 5;   // momentum, convert, five rounds of three products, apply
-
-// Muon's update of a batch of fp32 weights (matrices `stride` elements apart,
-// rows * cols a multiple of 4): the orthogonalised momentum scaled to the
-// root-mean-square of an AdamW step, 0.2 sqrt(max(rows, cols)).
-inline size_t update_workspace(int batch, int rows, int cols) {
-  Work w;
-  if (!plan(batch, rows, cols, &w)) return 0;
-  return w.total + (size_t)batch * rows * cols * 2;
-}
-
-inline int update(float* w, bf16* wb, float* g, float* mom, long stride, int batch, int rows, int cols, float lr,
-                  float mu, float wd, const float* gscale, const int* skip, void* ws, size_t ws_bytes, int* err,
-                  cudaStream_t s) {
-  Work wk;
-  if (!plan(batch, rows, cols, &wk) || ws_bytes < update_workspace(batch, rows, cols)) return GPT2_ERR_ARG;
-  const long count = (long)rows * cols;
-  if (count % 4 || stride % 4) return GPT2_ERR_ARG;
-  char* base = static_cast<char*>(ws);
-  bf16* o = reinterpret_cast<bf16*>(base + wk.total);
-  if (launch_pdl(momentum_kernel, dim3(wk.parts, batch), dim3(256), 0, s, g, mom, stride, count / 4, mu, gscale, skip,
-                 reinterpret_cast<double*>(base + wk.part)) != cudaSuccess)
-    return GPT2_ERR_CUDA;
-  const int st = orthogonalize<float>(g, stride, o, count, batch, rows, cols, 5, ws, wk.total, err, s, true);
-  if (st != GPT2_OK) return st;
-  const float adj = 0.2f * sqrtf((float)std::max(rows, cols));
-  return launch_pdl(apply_kernel, dim3(wk.parts, batch), dim3(256), 0, s, w, wb, g, (const bf16*)o, stride, count / 4,
-                    lr, adj, wd, skip) == cudaSuccess
-             ? GPT2_OK
-             : GPT2_ERR_CUDA;
+  __half* hi = reinterpret_cast<__half*>(base + w.x0);
+  __half* lo = reinterpret_cast<__half*>(base + w.lo);
+  uint32_t* count = reinterpret_cast<uint32_t*>(base + w.count);
+  const bool tall = rows > cols;
+  const int vec_rows = vec && (cols * sizeof(T)) % 16 == 0;   // every row of M begins on 16 bytes
+  const long work = tall ? (long)((w.n + 63) / 64) * (w.ld_x / 64) : ((long)w.n * w.ld_x / 8 + 255) / 256;
+  const int grid = (int)std::min(work, std::max(1L, 148L * 8 / batch));
+  return launch_pdl(tall ? ns_convert_kernel<T, true> : ns_convert_kernel<T, false>, dim3(grid, batch), dim3(256), 0, s,
+                    x, x_stride, rows, cols, (const double*)part, w.parts, hi, lo, w.ld_x, vec_rows, count);
 }
 
 }  // namespace muon

@@ -6,12 +6,12 @@
 // as hi and lo fp16. The
 // columns stand in blocks of 64: a block is 128 rows of 128 bytes in the 128-byte
 // swizzle, which is the K-major tile of X that X X^T wants and, read the other way,
-// the MN-major tile that Q X wants. A round is three products with their
+// the MN-major tile that P X wants. A round is three products with their
 // accumulators in tensor memory (128 x 128 twice, 128 x w) and three passes of
 // registers between tensor and shared memory. Only X X^T needs the other CTAs: each
 // sends its partial sum's columns to the CTA that adds them up (fp32, in the order
-// of the ranks), which sends the sum to all as fp16. A A and Q X^T's left operand are
-// formed by every CTA for itself.
+// of the ranks), which sends the sum to all as fp16. Every CTA
+// forms A A and P for itself.
 //
 // What bounds it is latency: about 15 dependent steps of 1 us. As separate launches
 // (two passes over M, then three products a round) the same work took 104 us for one
@@ -56,16 +56,6 @@ GPT2_DEV void unpack8(uint4 u, float* f) {
 GPT2_DEV uint4 pack8(const float* f) {
   return make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
 }
-// hi and lo of eight values
-GPT2_DEV void split8(const float* f, uint4& hi, uint4& lo) {
-  hi = pack8(f);
-  float h[8], l[8];
-  unpack8(hi, h);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) l[i] = f[i] - h[i];
-  lo = pack8(l);
-}
-
 GPT2_DEV void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 GPT2_DEV void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -92,8 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
   const int wb = a.w / 64;                         // blocks of this CTA's columns
   uint8_t* s_hi = smem;
   uint8_t* s_lo = s_hi + wb * kBlock;
-  uint8_t* s_q = s_lo + wb * kBlock;               // A, then Q
-  float* s_stage = reinterpret_cast<float*>(s_q + 2 * kBlock);
+  uint8_t* s_p = s_lo + wb * kBlock;               // A, then P
+  float* s_stage = reinterpret_cast<float*>(s_p + 2 * kBlock);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -181,12 +171,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
   }
 
   // ---- the rounds ------------------------------------------------------------------
-  // A A leaves its columns before Q X takes them
+  // A A leaves its columns before P X takes them
   const uint32_t d_gram = tmem, d_poly = tmem + 128, d_x = tmem + 128;
   const int q4 = warp & 3, group = warp >> 2;
   const int row = q4 * 32 + lane;
   const uint32_t t_row = (uint32_t)(q4 * 32) << 16;
-  const uint32_t hi32 = smem_u32(s_hi), q32 = smem_u32(s_q);
+  const uint32_t hi32 = smem_u32(s_hi), p32 = smem_u32(s_p);
   uint32_t phase = 0;
   // one thread issues a product once everything it reads is in shared memory
   auto product = [&](auto&& issue) {
@@ -222,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
         for (int i = 0; i < 32; ++i) v[i] *= kInvScale;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(s_q + (c >> 6) * kBlock + at_chunk(row, ((c & 63) >> 3) + j)) = pack8(v + 8 * j);
+          *reinterpret_cast<uint4*>(s_p + (c >> 6) * kBlock + at_chunk(row, ((c & 63) >> 3) + j)) = pack8(v + 8 * j);
       }
     } else {
       // columns [k span, ..) of the partial sum go to rank k: stage[source][4 columns][row]
@@ -254,18 +244,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
         for (int j = 0; j < 8; ++j) f[j] *= kInvScale;
         const uint4 h = pack8(f);
         const int col = rank * span + ch * 8;
-        const uint32_t o = q32 + (col >> 6) * kBlock + at_chunk(r, (col & 63) >> 3);
+        const uint32_t o = p32 + (col >> 6) * kBlock + at_chunk(r, (col & 63) >> 3);
         for (uint32_t k = 0; k < nc; ++k) st_cluster_v4(gemm2::mapa_shared(o, k), h);
       }
       fence_proxy_all();
       gemm2::cluster_sync();
     }
-    // Q = b A + c A A, in A's place
+    // P = a I + b A + c A A, in A's place
     product([&] {
       constexpr uint32_t idesc = idesc_f16_f32(128, 128, false);
       for (int kb = 0; kb < 2; ++kb)
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t d = smem_desc_sw128(q32 + kb * kBlock + kk * 32, 16, 1024);
+          const uint64_t d = smem_desc_sw128(p32 + kb * kBlock + kk * 32, 16, 1024);
           tc_mma_bf16(d_poly, d, d, idesc, (kb | kk) ? 1u : 0u);
         }
     });
@@ -275,21 +265,24 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
       tmem_ld32(d_poly + t_row + c, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint4* p = reinterpret_cast<uint4*>(s_q + (c >> 6) * kBlock + at_chunk(row, ((c & 63) >> 3) + j));
+        uint4* p = reinterpret_cast<uint4*>(s_p + (c >> 6) * kBlock + at_chunk(row, ((c & 63) >> 3) + j));
         float f[8];
         unpack8(*p, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fmaf(kB, f[i], kC * kInvScale * v[8 * j + i]);
+        for (int i = 0; i < 8; ++i) {
+          f[i] = fmaf(kB, f[i], kC * kInvScale * v[8 * j + i]);
+          if (c + 8 * j + i == row && row < a.n) f[i] += kA * kScale;
+        }
         *p = pack8(f);
       }
     }
-    // X <- a X + Q X
+    // X <- P X (+ a lo)
     product([&] {
       for (int c = 0; c < a.w; c += 256) {         // at most 256 columns an instruction
         const uint32_t idesc = idesc_f16_f32(128, min(256, a.w - c), true);
         for (int kb = 0; kb < 2; ++kb)
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(d_x + c, smem_desc_sw128(q32 + kb * kBlock + kk * 32, 16, 1024),
+            tc_mma_bf16(d_x + c, smem_desc_sw128(p32 + kb * kBlock + kk * 32, 16, 1024),
                         smem_desc_sw128(hi32 + (c >> 6) * kBlock + (kb * 64 + kk * 16) * 128, kBlock, 1024), idesc,
                         (kb | kk) ? 1u : 0u);
       }
@@ -301,11 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const T* __restri
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t o = (c >> 6) * kBlock + at_chunk(row, ((c & 63) >> 3) + j);
-        float f[8];
-        unpack8(*reinterpret_cast<const uint4*>(s_hi + o), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * j + i] = fmaf(kA, f[i], kInvScale * v[8 * j + i]);
+        for (int i = 0; i < 8; ++i) v[8 * j + i] *= kInvScale;
         if (use_lo) {
+          float f[8];
           unpack8(*reinterpret_cast<const uint4*>(s_lo + o), f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[8 * j + i] = fmaf(kA, f[i], v[8 * j + i]);

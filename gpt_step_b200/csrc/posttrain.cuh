@@ -70,177 +70,96 @@ GPT2_DEV void chunk_exp(uint4 u, float c, float2 (&e)[4]) {
   }
 }
 
-// A row held by the 32 G lanes of its warps, R chunks a lane (chunk i on lane i
-// mod 32 G): read once, its softmax and gradient from registers.
-template <int G, int R>
-struct HeldRow {
-  uint4 u[R];
-  int at;                                        // this lane's first chunk
-  GPT2_DEV HeldRow() : at(G == 1 ? (int)lane_id() : (int)threadIdx.x) {}
+// Two values rounded to bf16 on the fp32 pipe: x (2^16 + 1) - (x (2^16 + 1) - x) is x
+// rounded to 8 bits (Dekker's splitting), its upper half the bf16. The conversion
+// instruction shares the pipe of ex2, which is what bounds these kernels next to memory.
+// A value past 2^111 or a NaN becomes NaN, as its gradient row would be of no use.
+GPT2_DEV uint32_t round_bf16x2(float2 x) {
+  const float2 c = f2_mul(x, make_float2(65537.f, 65537.f));
+  const float2 d = f2_fma(x, make_float2(-1.f, -1.f), c);
+  const float2 h = f2_fma(d, make_float2(-1.f, -1.f), c);
+  return __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x7632);
+}
 
-  GPT2_DEV void load(const uint4* zr, int V) {
-    const int nv = (V + 7) / 8;
+// A chunk of the gradient g ([j == t] - 2^(y - c) / S), gs = -g / S; 0 behind the real columns.
+GPT2_DEV void store_chunk(uint4* dst, uint4 z, int col0, int t, int V, float c, float gs, float g) {
+  float2 e[4];
+  chunk_exp(z, c, e);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int i = at + q * 32 * G;
-      u[q] = i < nv ? __ldcs(zr + i) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
-    }
+  for (int j = 0; j < 4; ++j) e[j] = f2_mul(e[j], make_float2(gs, gs));
+  if (col0 + 8 > V || (unsigned)(t - col0) < 8u) {
+    // the target's chunk, and the last one, whose padded columns get exactly 0
+    float* f = &e[0].x;
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int i = at + q * 32 * G;
+    for (int j = 0; j < 8; ++j) f[j] = col0 + j >= V ? 0.f : f[j] + (col0 + j == t ? g : 0.f);
+  }
+  __stcs(dst, make_uint4(round_bf16x2(e[0]), round_bf16x2(e[1]), round_bf16x2(e[2]), round_bf16x2(e[3])));
+}
+
+// Columns from c0 on (a multiple of 8) of a gradient row, 0.
+GPT2_DEV void zero_row(uint4* dst, int c0, int Vp, int lane, int lanes) {
+  for (int i = c0 / 8 + lane; i < Vp / 8; i += lanes) __stcs(dst + i, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// (c, S) of a row read from global memory by the CTA's G warps, with its running maximum.
+template <int G>
+GPT2_DEV void streamed_stats(const uint4* zr, int V, float& c, float& s) {
+  constexpr int kThreads = 32 * G, kUnroll = 4;
+  c = -INFINITY;
+  s = 0.f;
+  const int nv = (V + 7) / 8;
+  for (int i0 = threadIdx.x; i0 < nv; i0 += kThreads * kUnroll) {
+    uint4 u[kUnroll];
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) {
+      const int i = i0 + q * kThreads;
+      u[q] = i < nv ? __ldcg(zr + i) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
       if (i == nv - 1) mask_chunk(u[q], i * 8, V);
     }
-  }
-
-  // max first, then one sum: no rescaling
-  GPT2_DEV void stats(float& c, float& s) const {
     __nv_bfloat162 m2 = chunk_max(u[0]);
 #pragma unroll
-    for (int q = 1; q < R; ++q) m2 = __hmax2(m2, chunk_max(u[q]));
+    for (int q = 1; q < kUnroll; ++q) m2 = __hmax2(m2, chunk_max(u[q]));
     const float2 mf = __bfloat1622float2(m2);
-    // the lanes of a warp share one c, so that their sums add up
-    c = warp_max(fmaxf(mf.x, mf.y)) * k::kLog2eF;
+    const float lm = fmaxf(mf.x, mf.y) * k::kLog2eF;
+    if (lm > c) {
+      s *= ex2_approx(c - lm);
+      c = lm;
+    }
     const float base = c == -INFINITY ? 0.f : c;
     float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
+    for (int q = 0; q < kUnroll; ++q) {
       float2 e[4];
       chunk_exp(u[q], base, e);
       acc0 = f2_add(acc0, f2_add(e[0], e[1]));
       acc1 = f2_add(acc1, f2_add(e[2], e[3]));
     }
-    s = warp_sum((acc0.x + acc0.y) + (acc1.x + acc1.y));
-    if (G > 1) combine_warps<G>(c, s);
+    s += (acc0.x + acc0.y) + (acc1.x + acc1.y);
   }
+  combine_stats<G>(c, s);
+}
 
-  // dst = g ([j == t] - 2^(y - c) / S), 0 behind the real columns
-  GPT2_DEV void gradient(uint4* dst, int t, int V, int Vp, float c, float s, float g) {
-    const float gs = -g / s;
-    const float2 gs2 = make_float2(gs, gs);
-    const int nv = Vp / 8;
-    // what is held over the reduction is the packed row, not its unpacked values
-    // (kept in fp32 by the compiler they took 248 registers a thread at R = 18)
+// A row's gradient from its (c, S), read from and written to global memory (dst may be the row).
+GPT2_DEV void streamed_gradient(const uint4* zr, uint4* dst, int t, int V, int Vp, float c, float s, float g, int lane,
+                                int lanes) {
+  constexpr int kUnroll = 4;
+  const float gs = -g / s;
+  const int nvr = (V + 7) / 8;
+  for (int i0 = lane; i0 < nvr; i0 += lanes * kUnroll) {
+    uint4 u[kUnroll];
 #pragma unroll
-    for (int q = 0; q < R; ++q)
-      asm volatile("" : "+r"(u[q].x), "+r"(u[q].y), "+r"(u[q].z), "+r"(u[q].w));
+    for (int q = 0; q < kUnroll; ++q) {
+      const int i = i0 + q * lanes;
+      u[q] = i < nvr ? __ldcs(zr + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int i = at + q * 32 * G;
-      if (i >= nv) break;
-      store_chunk(dst + i, u[q], i * 8, t, V, c, gs2, g);
+    for (int q = 0; q < kUnroll; ++q) {
+      const int i = i0 + q * lanes;
+      if (i < nvr) store_chunk(dst + i, u[q], i * 8, t, V, c, gs, g);
     }
   }
-
-  template <int GG>
-  static GPT2_DEV void combine_warps(float& c, float& s) {
-    __shared__ float2 red[GG];
-    if (lane_id() == 0) red[threadIdx.x >> 5] = make_float2(c, s);
-    __syncthreads();
-    c = red[0].x;
-    s = red[0].y;
-#pragma unroll
-    for (int w = 1; w < GG; ++w) k::ce_combine(c, s, red[w].x, red[w].y);
-  }
-
-  static GPT2_DEV void store_chunk(uint4* dst, uint4 z, int col0, int t, int V, float c, float2 gs2, float g) {
-    if (col0 >= V) {
-      __stcs(dst, make_uint4(0u, 0u, 0u, 0u));
-      return;
-    }
-    float2 e[4];
-    chunk_exp(z, c, e);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = f2_mul(e[j], gs2);
-    if (col0 + 8 > V || (unsigned)(t - col0) < 8u) {
-      // the target's chunk, and the last one, whose padded columns get exactly 0
-      float* f = &e[0].x;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = col0 + j >= V ? 0.f : f[j] + (col0 + j == t ? g : 0.f);
-    }
-    __stcs(dst, make_uint4(pack_bf16x2(e[0].x, e[0].y), pack_bf16x2(e[1].x, e[1].y), pack_bf16x2(e[2].x, e[2].y),
-                           pack_bf16x2(e[3].x, e[3].y)));
-  }
-};
-
-// A row too long for registers: streamed twice by the CTA's G warps, the second
-// time out of L2.
-template <int G>
-struct StreamedRow {
-  static constexpr int kThreads = 32 * G, kUnroll = 4;
-  const uint4* zr;
-
-  GPT2_DEV void load(const uint4* p, int) { zr = p; }
-
-  GPT2_DEV void stats_of(int V, float& c, float& s) const {
-    c = -INFINITY;
-    s = 0.f;
-    const int nv = (V + 7) / 8;
-    for (int i0 = threadIdx.x; i0 < nv; i0 += kThreads * kUnroll) {
-      uint4 u[kUnroll];
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        const int i = i0 + q * kThreads;
-        u[q] = i < nv ? __ldcg(zr + i) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
-        if (i == nv - 1) mask_chunk(u[q], i * 8, V);
-      }
-      __nv_bfloat162 m2 = chunk_max(u[0]);
-#pragma unroll
-      for (int q = 1; q < kUnroll; ++q) m2 = __hmax2(m2, chunk_max(u[q]));
-      const float2 mf = __bfloat1622float2(m2);
-      const float lm = fmaxf(mf.x, mf.y) * k::kLog2eF;
-      if (lm > c) {
-        s *= ex2_approx(c - lm);
-        c = lm;
-      }
-      const float base = c == -INFINITY ? 0.f : c;
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        float2 e[4];
-        chunk_exp(u[q], base, e);
-        acc0 = f2_add(acc0, f2_add(e[0], e[1]));
-        acc1 = f2_add(acc1, f2_add(e[2], e[3]));
-      }
-      s += (acc0.x + acc0.y) + (acc1.x + acc1.y);
-    }
-    combine_stats<G>(c, s);
-  }
-
-  GPT2_DEV void gradient(uint4* dst, int t, int V, int Vp, float c, float s, float g) const {
-    const float gs = -g / s;
-    const float2 gs2 = make_float2(gs, gs);
-    const int nv = Vp / 8;
-    for (int i0 = threadIdx.x; i0 < nv; i0 += kThreads * kUnroll) {
-      uint4 u[kUnroll];
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        const int i = i0 + q * kThreads;
-        u[q] = i * 8 < V ? __ldcs(zr + i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        const int i = i0 + q * kThreads;
-        if (i < nv) HeldRow<1, 1>::store_chunk(dst + i, u[q], i * 8, t, V, c, gs2, g);
-      }
-    }
-  }
-};
-
-// How a kernel's CTA holds its rows: R > 0: R chunks a lane of G warps; R == 0:
-// streamed by G warps. Several one-warp rows share a CTA of four warps.
-template <int G, int R>
-struct RowShape {
-  static constexpr int kRows = G == 1 ? 4 : 1;
-  static constexpr int kThreads = 32 * G * kRows;
-  // registers: the held chunks and about 50 more
-  static constexpr int kMinCtas = R > 0 ? 65536 / (kThreads * (4 * R + 50)) : 1;
-  static GPT2_DEV int row() { return G == 1 ? blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x; }
-  static GPT2_DEV bool first() { return G == 1 ? lane_id() == 0 : threadIdx.x == 0; }
-  static GPT2_DEV int lane() { return G == 1 ? lane_id() : threadIdx.x; }
-  static GPT2_DEV void zero(uint4* dst, int Vp) {
-    for (int i = lane(); i < Vp / 8; i += 32 * G) __stcs(dst + i, make_uint4(0u, 0u, 0u, 0u));
-  }
-};
+  zero_row(dst, nvr * 8, Vp, lane, lanes);
+}
 
 // (c, S) of a row from the logits GEMM's row partials (the same base-2 form).
 template <int G>
@@ -299,147 +218,245 @@ GPT2_DEV void policy_left_out(const PolicyArgs& a, int row, int t, bool first) {
 
 GPT2_DEV bool row_kept(int t, int V, int ignore_index) { return t != ignore_index && t >= 0 && t < V; }
 
-// A row: its softmax, the loss and g, the gradient. PART: (c, S) come from the
-// logits GEMM's partials and the row is read for the gradient alone.
-template <int G, int R, bool PART>
-__global__ void __launch_bounds__(RowShape<G, R>::kThreads, RowShape<G, R>::kMinCtas)
-    policy_loss_kernel(const PolicyArgs a) {
-  using Shape = RowShape<G, R>;
-  pdl_begin();
-  const int row = Shape::row();
-  if (row >= a.N) return;
-  const size_t off = (size_t)row * a.Vp;
-  const uint4* zr = reinterpret_cast<const uint4*>(a.logits + off);
-  uint4* dr = a.dlogits ? reinterpret_cast<uint4*>(a.dlogits + off) : nullptr;
-  const int t = a.targets[row];
-  if (!row_kept(t, a.V, a.ignore_index)) {
-    policy_left_out(a, row, t, Shape::first());
-    if (dr) Shape::zero(dr, a.Vp);
-    return;
-  }
-  std::conditional_t<(R > 0), HeldRow<G, R ? R : 1>, StreamedRow<G>> held;
-  held.load(zr, a.V);
-  const float old_lp = a.old_logp[row], adv = a.adv[row];
-  const float ref = a.ref_logp ? a.ref_logp[row] : 0.f;
-  const float w = a.weight ? a.weight[row] : 1.f;
-  const float zt = __bfloat162float(a.logits[off + t]);   // before any thread may overwrite it
-  float c, s, loss, g;
-  if constexpr (PART) part_stats<G>(a.part + (size_t)row * a.slots, a.slots, Shape::lane(), c, s);
-  else if constexpr (R > 0) held.stats(c, s);
-  else held.stats_of(a.V, c, s);
-  const float lp = row_logp(zt, c, s);
-  policy_row(a, lp, old_lp, adv, ref, w, loss, g);
-  if (Shape::first()) {
-    a.losses[row] = loss;
-    if (a.logps) a.logps[row] = lp;
-  }
-  if (!dr) return;
-  if (g == 0.f && isfinite(lp)) Shape::zero(dr, a.Vp);
-  else held.gradient(dr, t, a.V, a.Vp, c, s, g);
-}
-
 GPT2_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 GPT2_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Long rows, persistent: a row stands in shared memory, every chunk in a slot of
-// the thread that works on it, so a chunk's slot takes the next row's chunk as
-// soon as its gradient is formed, with no barrier between; the copy of a row runs
-// under the gradient and the stores of the one before. The sum takes the target's
-// logit as its reference: 2^(y - y_t) needs no pass for the maximum, and a row
+// The rows of a CTA, in windows of 32, row k of the window with lane k. Of every gridDim.x
+// rows a CTA takes one, each time 0.38 of the way further on: with a fixed place, sequences
+// whose length divides the grid would give all their prompts (rows left out) to the same
+// CTAs. A window's targets, and with them the targets' logits, are read 32 at a time.
+struct RowWindows {
+  const int32_t* targets;
+  const bf16* logits;
+  long begin, end, base;            // rows of interest; the window's first row number without the turn
+  int V, Vp, ignore_index;
+  uint32_t grid, place, lane_turn, turn32, hits;
+  long row;                         // this lane's row and its target and logit
+  int t;
+  float zt;
+
+  GPT2_DEV RowWindows(const int32_t* tg, const bf16* z, long b, long e, int v, int vp, int ign)
+      : targets(tg), logits(z), begin(b), end(e), V(v), Vp(vp), ignore_index(ign), hits(0), row(0), t(0), zt(0.f) {
+    grid = gridDim.x;
+    const uint32_t turn = (uint32_t)(0.382f * grid);
+    lane_turn = lane_id() * turn % grid;
+    turn32 = 32 * turn % grid;
+    base = 0;
+    place = blockIdx.x;
+  }
+  GPT2_DEV bool more() const { return base < end; }
+  // Reads the next window; the lanes whose row is of interest but left out.
+  GPT2_DEV uint32_t load() {
+    uint32_t at = place + lane_turn;
+    if (at >= grid) at -= grid;
+    row = base + (long)lane_id() * grid + at;
+    const bool in = row >= begin && row < end;
+    t = in ? targets[row] : -1;
+    const bool kept = in && row_kept(t, V, ignore_index);
+    zt = kept ? __bfloat162float(logits[(size_t)row * Vp + t]) : 0.f;
+    hits = __ballot_sync(0xffffffffu, kept);
+    base += 32L * grid;
+    place += turn32;
+    if (place >= grid) place -= grid;
+    return __ballot_sync(0xffffffffu, in && !kept);
+  }
+};
+
+// A row in shared memory: every 16-byte chunk has a slot that belongs to the thread that
+// works on it, so a slot takes the next row's chunk as soon as this row is done with it,
+// without a barrier, and copies run under the arithmetic and the stores. The sum takes the
+// target's logit as its reference, c = y_t, which needs no pass for the maximum; a row
 // where that overflows is summed again from its maximum.
 template <int G>
-__global__ void __launch_bounds__(32 * G, 32 / G) policy_long_kernel(const PolicyArgs a) {
-  constexpr int kT = 32 * G;
-  extern __shared__ __align__(128) uint4 slots[];
+struct RowPipe {
+  static constexpr int kThreads = 32 * G;
+  uint4* slots;
+  uint32_t slot0;
+  int nvr;                       // chunks that hold real ids
+  float (*red)[G];               // [2][G]: two sums in flight
+  int flip;
+
+  GPT2_DEV void prefetch(const uint4* zr) const {
+    for (int i = threadIdx.x; i < nvr; i += kThreads) cp_async16(slot0 + i * 16, zr + i);
+  }
+  // Waits for this thread's chunks of the row.
+  GPT2_DEV void arrive(int V) const {
+    cp_async_wait();
+    if ((nvr - 1) % kThreads == (int)threadIdx.x) mask_chunk(slots[nvr - 1], (nvr - 1) * 8, V);
+  }
+  GPT2_DEV float sum_all(float v) {
+    v = warp_sum(v);
+    if (G == 1) return v;
+    if (lane_id() == 0) red[flip][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane_id() < G ? red[flip][lane_id()] : 0.f;
+    flip ^= 1;
+    return warp_sum(v);
+  }
+  // sum of 2^(y - c); with `zn` the slots take the next row on the way.
+  GPT2_DEV float sum_from(float c, const uint4* zn) {
+    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+    auto add = [&](uint4 u) {
+      float2 e[4];
+      chunk_exp(u, c, e);
+      acc0 = f2_add(acc0, f2_add(e[0], e[1]));
+      acc1 = f2_add(acc1, f2_add(e[2], e[3]));
+    };
+    int i = threadIdx.x;
+    for (; i + 3 * kThreads < nvr; i += 4 * kThreads) {   // four chunks in flight
+      uint4 u[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u[q] = slots[i + q * kThreads];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) add(u[q]);
+      if (zn) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cp_async16(slot0 + (i + q * kThreads) * 16, zn + i + q * kThreads);
+      }
+    }
+    for (; i < nvr; i += kThreads) {
+      add(slots[i]);
+      if (zn) cp_async16(slot0 + i * 16, zn + i);
+    }
+    return sum_all((acc0.x + acc0.y) + (acc1.x + acc1.y));
+  }
+};
+
+template <int G>
+__global__ void __launch_bounds__(32 * G, 32 / G) policy_loss_kernel(const PolicyArgs a) {
+  extern __shared__ __align__(128) uint4 row_slots[];
   __shared__ float red[2][G];
   __shared__ float red_m[G];
   pdl_begin();
-  const int stride = gridDim.x, nvr = (a.V + 7) / 8, nv = a.Vp / 8;
-  const int lane = lane_id(), warp = threadIdx.x >> 5;
-  auto kept_at = [&](long r) { return r < a.N && row_kept(a.targets[r], a.V, a.ignore_index); };
-  // the first kept row of r, r + stride, ..., or one past the last row
-  auto scan = [&](long r) {
-    for (; r < a.N; r += 32L * stride) {
-      const uint32_t hit = __ballot_sync(0xffffffffu, kept_at(r + (long)lane * stride));
-      if (hit) return r + (long)(__ffs(hit) - 1) * stride;
+  const int lane = lane_id();
+  RowPipe<G> pipe{row_slots, smem_u32(row_slots), (a.V + 7) / 8, red, 0};
+  RowWindows win(a.targets, a.logits, 0, a.N, a.V, a.Vp, a.ignore_index);
+  float l_old = 0.f, l_adv = 0.f, l_ref = 0.f, l_w = 1.f;   // of the lane's row
+  // The next kept row's lane in the window, -1 behind the last; rows left out on the way are finished.
+  auto advance = [&]() {
+    while (win.hits == 0) {
+      if (!win.more()) return -1;
+      for (uint32_t miss = win.load(); miss; miss &= miss - 1) {
+        const long r = __shfl_sync(0xffffffffu, win.row, __ffs(miss) - 1);
+        policy_left_out(a, (int)r, a.targets[r], threadIdx.x == 0);
+        if (a.dlogits) zero_row(reinterpret_cast<uint4*>(a.dlogits + (size_t)r * a.Vp), 0, a.Vp, threadIdx.x, 32 * G);
+      }
+      if (win.hits >> lane & 1) {
+        l_old = a.old_logp[win.row];
+        l_adv = a.adv[win.row];
+        if (a.ref_logp) l_ref = a.ref_logp[win.row];
+        if (a.weight) l_w = a.weight[win.row];
+      }
     }
+    const int j = __ffs(win.hits) - 1;
+    win.hits &= win.hits - 1;
+    return j;
+  };
+  // a row's numbers, from the lane that has them
+  struct Row { long row; int t; float zt, old_lp, adv, ref, w; };
+  auto take = [&](int j) {
+    Row r;
+    r.row = __shfl_sync(0xffffffffu, win.row, j);
+    r.t = __shfl_sync(0xffffffffu, win.t, j);
+    r.zt = __shfl_sync(0xffffffffu, win.zt, j);
+    r.old_lp = __shfl_sync(0xffffffffu, l_old, j);
+    r.adv = __shfl_sync(0xffffffffu, l_adv, j);
+    r.ref = __shfl_sync(0xffffffffu, l_ref, j);
+    r.w = __shfl_sync(0xffffffffu, l_w, j);
     return r;
   };
-  auto skip = [&](long from, long to) {
-    for (long r = from; r < to && r < a.N; r += stride) {
-      policy_left_out(a, (int)r, a.targets[r], threadIdx.x == 0);
-      if (a.dlogits) RowShape<G, 0>::zero(reinterpret_cast<uint4*>(a.dlogits + (size_t)r * a.Vp), a.Vp);
-    }
-  };
-  const uint32_t slot0 = smem_u32(slots);
-  long row = scan(blockIdx.x);
-  if (row < a.N) {
-    const uint4* zr = reinterpret_cast<const uint4*>(a.logits + (size_t)row * a.Vp);
-    for (int i = threadIdx.x; i < nvr; i += kT) cp_async16(slot0 + i * 16, zr + i);
-  }
-  skip(blockIdx.x, row);
-  int flip = 0;
-  while (row < a.N) {
+  int j = advance();
+  if (j < 0) return;
+  Row cur = take(j);
+  pipe.prefetch(reinterpret_cast<const uint4*>(a.logits + (size_t)cur.row * a.Vp));
+  while (j >= 0) {
+    const long row = cur.row;
     const size_t off = (size_t)row * a.Vp;
-    const int t = a.targets[row];
-    const float zt = __bfloat162float(a.logits[off + t]);   // before any thread may overwrite it
-    const float old_lp = a.old_logp[row], adv = a.adv[row];
-    const float ref = a.ref_logp ? a.ref_logp[row] : 0.f;
-    const float w = a.weight ? a.weight[row] : 1.f;
-    const long next = scan(row + stride);
-    cp_async_wait();
-    if ((nvr - 1) % kT == (int)threadIdx.x) mask_chunk(slots[nvr - 1], (nvr - 1) * 8, a.V);
-    auto sum_from = [&](float c) {
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < nvr; i += kT) {
-        float2 e[4];
-        chunk_exp(slots[i], c, e);
-        acc0 = f2_add(acc0, f2_add(e[0], e[1]));
-        acc1 = f2_add(acc1, f2_add(e[2], e[3]));
-      }
-      const float p = warp_sum((acc0.x + acc0.y) + (acc1.x + acc1.y));
-      if (lane == 0) red[flip][warp] = p;
-      __syncthreads();
-      const float v = lane < G ? red[flip][lane] : 0.f;
-      flip ^= 1;
-      return warp_sum(v);
-    };
-    float c = zt * k::kLog2eF, s = sum_from(c);
+    const int t = cur.t;
+    const float zt = cur.zt;
+    pipe.arrive(a.V);
+    float c = zt * k::kLog2eF, s = pipe.sum_from(c, nullptr);
     if (!(s < 3e38f)) {   // (the same in every thread)
       __nv_bfloat162 m2 = as_bf2(kNegInf2);
-      for (int i = threadIdx.x; i < nvr; i += kT) m2 = __hmax2(m2, chunk_max(slots[i]));
+      for (int i = threadIdx.x; i < pipe.nvr; i += 32 * G) m2 = __hmax2(m2, chunk_max(row_slots[i]));
       const float2 mf = __bfloat1622float2(m2);
-      const float m = warp_max(fmaxf(mf.x, mf.y));
-      if (lane == 0) red_m[warp] = m;
-      __syncthreads();
-      c = warp_max(lane < G ? red_m[lane] : -INFINITY) * k::kLog2eF;
-      s = sum_from(c);
+      float m = warp_max(fmaxf(mf.x, mf.y));
+      if (G > 1) {
+        if (lane == 0) red_m[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = warp_max(lane < G ? red_m[lane] : -INFINITY);
+      }
+      c = m * k::kLog2eF;
+      s = pipe.sum_from(c, nullptr);
     }
     const float lp = row_logp(zt, c, s);
     float loss, g;
-    policy_row(a, lp, old_lp, adv, ref, w, loss, g);
+    policy_row(a, lp, cur.old_lp, cur.adv, cur.ref, cur.w, loss, g);
     if (threadIdx.x == 0) {
       a.losses[row] = loss;
       if (a.logps) a.logps[row] = lp;
     }
+    j = advance();
+    if (j >= 0) cur = take(j);
     uint4* dr = a.dlogits ? reinterpret_cast<uint4*>(a.dlogits + off) : nullptr;
-    const uint4* zn = next < a.N ? reinterpret_cast<const uint4*>(a.logits + (size_t)next * a.Vp) : nullptr;
+    const uint4* zn = j >= 0 ? reinterpret_cast<const uint4*>(a.logits + (size_t)cur.row * a.Vp) : nullptr;
     const bool none = !dr || (g == 0.f && isfinite(lp));
     const float gs = -g / s;
-    const float2 gs2 = make_float2(gs, gs);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < nvr; i += kT) {
-      if (!none) HeldRow<1, 1>::store_chunk(dr + i, slots[i], i * 8, t, a.V, c, gs2, g);
-      if (zn) cp_async16(slot0 + i * 16, zn + i);
+    if (none) {
+      if (zn) pipe.prefetch(zn);
+    } else {
+      constexpr int kT = 32 * G;
+      int i = threadIdx.x;
+      for (; i + kT < pipe.nvr; i += 2 * kT) {   // two chunks in flight
+        const uint4 u0 = row_slots[i], u1 = row_slots[i + kT];
+        store_chunk(dr + i, u0, i * 8, t, a.V, c, gs, g);
+        store_chunk(dr + i + kT, u1, (i + kT) * 8, t, a.V, c, gs, g);
+        if (zn) {
+          cp_async16(pipe.slot0 + i * 16, zn + i);
+          cp_async16(pipe.slot0 + (i + kT) * 16, zn + i + kT);
+        }
+      }
+      if (i < pipe.nvr) {
+        store_chunk(dr + i, row_slots[i], i * 8, t, a.V, c, gs, g);
+        if (zn) cp_async16(pipe.slot0 + i * 16, zn + i);
+      }
     }
-    if (dr)
-      for (int i = (none ? 0 : nvr) + threadIdx.x; i < nv; i += kT) __stcs(dr + i, make_uint4(0u, 0u, 0u, 0u));
-    skip(row + stride, next);
-    row = next;
+    if (dr) zero_row(dr, none ? 0 : pipe.nvr * 8, a.Vp, threadIdx.x, 32 * G);
   }
+}
+
+// A row a CTA, from global memory: rows too long for shared memory (read a second time
+// for the gradient, out of L2), and with PART rows whose (c, S) the logits GEMM's
+// epilogue has left, which are read for the gradient alone.
+template <int G, bool PART>
+__global__ void __launch_bounds__(32 * G) policy_streamed_kernel(const PolicyArgs a) {
+  pdl_begin();
+  const int row = blockIdx.x;
+  const size_t off = (size_t)row * a.Vp;
+  const uint4* zr = reinterpret_cast<const uint4*>(a.logits + off);
+  uint4* dr = a.dlogits ? reinterpret_cast<uint4*>(a.dlogits + off) : nullptr;
+  const int t = a.targets[row];
+  if (!row_kept(t, a.V, a.ignore_index)) {
+    policy_left_out(a, row, t, threadIdx.x == 0);
+    if (dr) zero_row(dr, 0, a.Vp, threadIdx.x, 32 * G);
+    return;
+  }
+  const float zt = __bfloat162float(a.logits[off + t]);   // before any thread may overwrite it
+  float c, s, loss, g;
+  if (PART) part_stats<G>(a.part + (size_t)row * a.slots, a.slots, threadIdx.x, c, s);
+  else streamed_stats<G>(zr, a.V, c, s);
+  const float lp = row_logp(zt, c, s);
+  policy_row(a, lp, a.old_logp[row], a.adv[row], a.ref_logp ? a.ref_logp[row] : 0.f, a.weight ? a.weight[row] : 1.f,
+             loss, g);
+  if (threadIdx.x == 0) {
+    a.losses[row] = loss;
+    if (a.logps) a.logps[row] = lp;
+  }
+  if (!dr) return;
+  if (g == 0.f && isfinite(lp)) zero_row(dr, 0, a.Vp, threadIdx.x, 32 * G);
+  else streamed_gradient(zr, dr, t, a.V, a.Vp, c, s, g, threadIdx.x, 32 * G);
 }
 
 struct RowArgs {
@@ -454,35 +471,75 @@ struct RowArgs {
   int* err;
 };
 
-// A row's lp (0 for a row left out) and (c, S).
-template <int G, int R, bool PART>
-__global__ void __launch_bounds__(RowShape<G, R>::kThreads) row_logp_kernel(const RowArgs a) {
-  using Shape = RowShape<G, R>;
+// Rows' lp (0 for rows left out) and (c, S); rows outside the sequences are passed over.
+template <int G>
+__global__ void __launch_bounds__(32 * G, 32 / G) row_logp_kernel(const RowArgs a) {
+  extern __shared__ __align__(128) uint4 row_slots[];
+  __shared__ float red[2][G];
   pdl_begin();
-  const int row = Shape::row();
-  if (row >= a.N) return;
+  RowPipe<G> pipe{row_slots, smem_u32(row_slots), (a.V + 7) / 8, red, 0};
+  long begin = 0, end = a.N;
+  if (a.seq_start) {
+    begin = a.seq_start[0];
+    end = min(end, (long)a.seq_start[a.n_seq]);
+  }
+  RowWindows win(a.targets, a.logits, begin, end, a.V, a.Vp, a.ignore_index);
+  auto advance = [&]() {
+    while (win.hits == 0) {
+      if (!win.more()) return -1;
+      if (win.load() >> lane_id() & 1) {
+        if (win.t != a.ignore_index) atomicOr(a.err, DEVERR_TOKEN_RANGE);
+        a.logps[win.row] = 0.f;
+      }
+    }
+    const int j = __ffs(win.hits) - 1;
+    win.hits &= win.hits - 1;
+    return j;
+  };
+  int j = advance();
+  if (j < 0) return;
+  long row = __shfl_sync(0xffffffffu, win.row, j);
+  float zt = __shfl_sync(0xffffffffu, win.zt, j);
+  pipe.prefetch(reinterpret_cast<const uint4*>(a.logits + (size_t)row * a.Vp));
+  while (j >= 0) {
+    j = advance();
+    const long next = __shfl_sync(0xffffffffu, win.row, max(j, 0));
+    const float zt_next = __shfl_sync(0xffffffffu, win.zt, max(j, 0));
+    const uint4* zn = j >= 0 ? reinterpret_cast<const uint4*>(a.logits + (size_t)next * a.Vp) : nullptr;
+    pipe.arrive(a.V);
+    float c = zt * k::kLog2eF, s = pipe.sum_from(c, zn);
+    if (!(s < 3e38f))   // (the same in every thread) the slots have moved on
+      streamed_stats<G>(reinterpret_cast<const uint4*>(a.logits + (size_t)row * a.Vp), a.V, c, s);
+    if (threadIdx.x == 0) {
+      a.logps[row] = row_logp(zt, c, s);
+      if (a.stats) a.stats[row] = make_float2(c, s);
+    }
+    row = next;
+    zt = zt_next;
+  }
+}
+
+// The same a row a CTA: rows too long for shared memory, and with PART rows whose (c, S)
+// the logits GEMM's epilogue has left (the target's logit too where none are stored).
+template <int G, bool PART>
+__global__ void __launch_bounds__(32 * G) row_logp_streamed_kernel(const RowArgs a) {
+  pdl_begin();
+  const int row = blockIdx.x;
   if (a.seq_start && (row < a.seq_start[0] || row >= a.seq_start[a.n_seq])) return;
   const size_t off = (size_t)row * a.Vp;
   const int t = a.targets[row];
-  const bool in_range = t >= 0 && t < a.V;
-  if (t == a.ignore_index || !in_range) {
-    if (Shape::first()) {
+  if (!row_kept(t, a.V, a.ignore_index)) {
+    if (threadIdx.x == 0) {
       if (t != a.ignore_index) atomicOr(a.err, DEVERR_TOKEN_RANGE);
       a.logps[row] = 0.f;
     }
     return;
   }
-  float c, s;
   const float zt = a.tgt_val ? a.tgt_val[row] : __bfloat162float(a.logits[off + t]);
-  if constexpr (PART) {
-    part_stats<G>(a.part + (size_t)row * a.slots, a.slots, Shape::lane(), c, s);
-  } else {
-    std::conditional_t<(R > 0), HeldRow<G, R ? R : 1>, StreamedRow<G>> held;
-    held.load(reinterpret_cast<const uint4*>(a.logits + off), a.V);
-    if constexpr (R > 0) held.stats(c, s);
-    else held.stats_of(a.V, c, s);
-  }
-  if (Shape::first()) {
+  float c, s;
+  if (PART) part_stats<G>(a.part + (size_t)row * a.slots, a.slots, threadIdx.x, c, s);
+  else streamed_stats<G>(reinterpret_cast<const uint4*>(a.logits + off), a.V, c, s);
+  if (threadIdx.x == 0) {
     a.logps[row] = row_logp(zt, c, s);
     if (a.stats) a.stats[row] = make_float2(c, s);
   }
@@ -500,8 +557,6 @@ struct PairArgs {
   float beta, smoothing, dscale;
   int* err;
 };
-
-GPT2_DEV double softplus_d(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
 
 // One CTA per pair. Sequence 2p is the chosen one, 2p + 1 the rejected one. The
 // sums over a sequence and the difference of the two run in 64 bits: a margin
@@ -528,13 +583,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
     }
     double s = 0.0;
     int n = 0;
-    for (int i = b + threadIdx.x; i < e; i += kPairThreads) {
-      const int t = a.targets[i];
-      if (t != a.ignore_index && t >= 0 && t < a.V) {
-        s += (double)a.logps[i];
-        ++n;
-      }
-    }
+#pragma unroll 4
+    for (int i = b + threadIdx.x; i < e; i += kPairThreads) s += (double)a.logps[i];   // 0 for rows left out
+    if (a.average)
+      for (int i = b + threadIdx.x; i < e; i += kPairThreads) n += row_kept(a.targets[i], a.V, a.ignore_index);
     s = warp_sum_d(s);
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane_id() == 0) {
@@ -560,8 +612,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   const double delta = gap[0] - gap[1], b = a.beta, eps = a.smoothing;
   double loss, dd;
   if (a.kind == 0) {
-    loss = (1.0 - eps) * softplus_d(-b * delta) + eps * softplus_d(b * delta);
-    dd = -b * ((1.0 - eps) / (1.0 + exp(b * delta)) - eps / (1.0 + exp(-b * delta)));
+    // softplus(+-x) and sigma(+-x) from one exponential
+    const double x = b * delta, e = exp(-fabs(x)), l = log1p(e), big = 1.0 / (1.0 + e), small = e * big;
+    const double up = fmax(-x, 0.0) + l, down = fmax(x, 0.0) + l;   // softplus(-x), softplus(x)
+    loss = (1.0 - eps) * up + eps * down;
+    dd = -b * (x > 0 ? (1.0 - eps) * small - eps * big : (1.0 - eps) * big - eps * small);
   } else {
     const double off = delta - 0.5 / b;
     loss = off * off;
@@ -597,41 +652,26 @@ GPT2_DEV int find_sequence(const int32_t* start, int n_seq, int row) {
   return (lo > 0 && row < start[lo]) ? lo - 1 : -1;
 }
 
-// A row's gradient, from the pair's coefficient and the row's (c, S).
+// Rows' gradients from their pair's coefficient and their (c, S): a warp a row where G is
+// 1 (four a CTA), else the CTA's G warps.
 template <int G>
-__global__ void __launch_bounds__(RowShape<G, 0>::kThreads) pair_grad_kernel(const PairGradArgs a) {
-  using Shape = RowShape<G, 0>;
+__global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const PairGradArgs a) {
   pdl_begin();
-  const int row = Shape::row();
+  const int row = G == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int lane = G == 1 ? lane_id() : threadIdx.x;
   if (row >= a.N) return;
   const int seq = a.seq_start ? find_sequence(a.seq_start, a.n_seq, row) : row / a.seq_len;
   if (seq < 0 || seq >= a.n_seq) return;   // behind the last sequence: left as it was
   const size_t off = (size_t)row * a.Vp;
   uint4* dr = reinterpret_cast<uint4*>(a.dlogits + off);
   const int t = a.targets[row];
-  if (t == a.ignore_index || t < 0 || t >= a.V) {
-    Shape::zero(dr, a.Vp);
+  if (!row_kept(t, a.V, a.ignore_index)) {
+    zero_row(dr, 0, a.Vp, lane, 32 * G);
     return;
   }
   const float2 st = a.stats[row];
-  const uint4* zr = reinterpret_cast<const uint4*>(a.logits + off);
-  const float g = a.coef[seq], gs = -g / st.y;
-  const float2 gs2 = make_float2(gs, gs);
-  const int nv = a.Vp / 8;
-  constexpr int kStep = 32 * G, kUnroll = 4;
-  for (int i0 = Shape::lane(); i0 < nv; i0 += kStep * kUnroll) {
-    uint4 u[kUnroll];
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q) {
-      const int i = i0 + q * kStep;
-      u[q] = i * 8 < a.V ? __ldcs(zr + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q) {
-      const int i = i0 + q * kStep;
-      if (i < nv) HeldRow<1, 1>::store_chunk(dr + i, u[q], i * 8, t, a.V, st.x, gs2, g);
-    }
-  }
+  streamed_gradient(reinterpret_cast<const uint4*>(a.logits + off), dr, t, a.V, a.Vp, st.x, st.y, a.coef[seq], lane,
+                    32 * G);
 }
 
 // acc += factor * rows * sum(losses), *mean_out = factor * sum(losses) (fp64 sums).
@@ -663,73 +703,70 @@ inline bool logits_ok(const void* logits, int N, int V, int Vp) {
   return N > 0 && V > 0 && V <= Vp && Vp % 8 == 0 && aligned16(logits);
 }
 
+constexpr int kSmemSm = 227 * 1024, kSmemCta = 1024 + 512;   // of an SM; a CTA's own share beside its row
+
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// Calls f(G, R) with the shape that holds a row of Vp columns, or (0, 0).
+// Calls f(G) with the fewest warps for one row of V ids in shared memory that keep 32 warps
+// an SM at work on the rows it holds: f(0) where one row does not fit.
 template <typename F>
-int with_shape(int Vp, F&& f) {
-  const int nv = Vp / 8;
-  if (nv <= 4 * 32) return f(Int<1>{}, Int<4>{});
-  if (nv <= 10 * 32) return f(Int<1>{}, Int<10>{});
-  if (nv <= 18 * 32) return f(Int<1>{}, Int<18>{});
-  if (nv <= 9 * 128) return f(Int<4>{}, Int<9>{});
-  if (nv <= 16 * 128) return f(Int<4>{}, Int<16>{});
-  if (nv <= 16 * 256) return f(Int<8>{}, Int<16>{});
-  return f(Int<0>{}, Int<0>{});
+int with_warps(int V, F&& f) {
+  const int bytes = (V + 7) / 8 * 16 + kSmemCta;
+  if (bytes * 32 <= kSmemSm) return f(Int<1>{});
+  if (bytes * 16 <= kSmemSm) return f(Int<2>{});
+  if (bytes * 8 <= kSmemSm) return f(Int<4>{});
+  if (bytes * 4 <= kSmemSm) return f(Int<8>{});
+  if (bytes * 2 <= kSmemSm) return f(Int<16>{});
+  if (bytes <= kSmemSm) return f(Int<32>{});
+  return f(Int<0>{});
 }
 
-constexpr int kLongMax = 112 * 1024;   // shared memory of one of two CTAs an SM
-
-template <int G, int R, typename... KArgs, typename Args>
-int launch_rows(void (*kern)(KArgs...), int N, cudaStream_t s, const Args& a) {
-  using Shape = RowShape<G, R>;
-  const int grid = (N + Shape::kRows - 1) / Shape::kRows;
-  return launch_pdl(kern, dim3(grid), dim3(Shape::kThreads), 0, s, a) == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
+template <int G, typename Args>
+int launch_pipe(void (*kern)(Args), const Args& a, PerDeviceOnce& once, cudaStream_t s) {
+  if (smem_optin(once, kern, kSmemSm - kSmemCta) != cudaSuccess) return GPT2_ERR_CUDA;
+  const int bytes = (a.V + 7) / 8 * 16;
+  const int per_sm = std::min(32 / G, kSmemSm / (bytes + kSmemCta));
+  const int grid = std::min(a.N, device_sm_count() * per_sm);
+  return launch_pdl(kern, dim3(grid), dim3(32 * G), bytes, s, a) == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
 }
 
-template <int G>
-int launch_long(const PolicyArgs& a, cudaStream_t s) {
-  static PerDeviceOnce once;
-  if (smem_optin(once, policy_long_kernel<G>, kLongMax * (G / 16)) != cudaSuccess) return GPT2_ERR_CUDA;
-  const int grid = std::min(a.N, device_sm_count() * (32 / G));
-  return launch_pdl(policy_long_kernel<G>, dim3(grid), dim3(32 * G), (a.V + 7) / 8 * 16, s, a) == cudaSuccess
-             ? GPT2_OK
-             : GPT2_ERR_CUDA;
-}
+inline int launched(cudaError_t e) { return e == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA; }
 
 inline int policy_loss(const PolicyArgs& a, cudaStream_t s) {
-  if (a.part) return launch_rows<8, 0>(policy_loss_kernel<8, 0, true>, a.N, s, a);
-  return with_shape(a.Vp, [&](auto g, auto r) {
-    constexpr int G = decltype(g)::value, R = decltype(r)::value;
+  if (a.part) return launched(launch_pdl(policy_streamed_kernel<8, true>, dim3(a.N), dim3(256), 0, s, a));
+  return with_warps(a.V, [&](auto g) {
+    constexpr int G = decltype(g)::value;
     if constexpr (G > 0) {
-      return launch_rows<G, R>(policy_loss_kernel<G, R, false>, a.N, s, a);
+      static PerDeviceOnce once;
+      return launch_pipe<G>(policy_loss_kernel<G>, a, once, s);
     } else {
-      const int bytes = (a.V + 7) / 8 * 16;
-      if (bytes <= kLongMax) return launch_long<16>(a, s);
-      if (bytes <= 2 * kLongMax) return launch_long<32>(a, s);
-      return launch_rows<16, 0>(policy_loss_kernel<16, 0, false>, a.N, s, a);
+      return launched(launch_pdl(policy_streamed_kernel<16, false>, dim3(a.N), dim3(512), 0, s, a));
     }
   });
 }
 
 inline int row_logps(const RowArgs& a, cudaStream_t s) {
-  if (a.part) return launch_rows<1, 0>(row_logp_kernel<1, 0, true>, a.N, s, a);
-  return with_shape(a.Vp, [&](auto g, auto r) {
-    constexpr int G = decltype(g)::value, R = decltype(r)::value;
-    if constexpr (G > 0) return launch_rows<G, R>(row_logp_kernel<G, R, false>, a.N, s, a);
-    else return launch_rows<8, 0>(row_logp_kernel<8, 0, false>, a.N, s, a);
+  if (a.part) return launched(launch_pdl(row_logp_streamed_kernel<1, true>, dim3(a.N), dim3(32), 0, s, a));
+  return with_warps(a.V, [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    if constexpr (G > 0) {
+      static PerDeviceOnce once;
+      return launch_pipe<G>(row_logp_kernel<G>, a, once, s);
+    } else {
+      return launched(launch_pdl(row_logp_streamed_kernel<16, false>, dim3(a.N), dim3(512), 0, s, a));
+    }
   });
 }
 
 inline int pair_losses(const PairArgs& a, int P, cudaStream_t s) {
-  return launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, a) == cudaSuccess ? GPT2_OK : GPT2_ERR_CUDA;
+  return launched(launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, a));
 }
 
 inline int pair_gradients(const PairGradArgs& a, cudaStream_t s) {
-  if (a.Vp <= 4608) return launch_rows<1, 0>(pair_grad_kernel<1>, a.N, s, a);
-  if (a.Vp <= 16384) return launch_rows<4, 0>(pair_grad_kernel<4>, a.N, s, a);
-  return launch_rows<8, 0>(pair_grad_kernel<8>, a.N, s, a);
+  if (a.Vp <= 4608) return launched(launch_pdl(pair_grad_kernel<1>, dim3((a.N + 3) / 4), dim3(128), 0, s, a));
+  if (a.Vp <= 16384) return launched(launch_pdl(pair_grad_kernel<4>, dim3(a.N), dim3(128), 0, s, a));
+  return launched(launch_pdl(pair_grad_kernel<8>, dim3(a.N), dim3(256), 0, s, a));
 }
 
 // Workspace: a row's (c, S), then a sequence's coefficient.

@@ -1210,11 +1210,12 @@ int gpt2_clip_muon(gpt2_model* m, int32_t step, float momentum, void* workspace,
     if (d.L == 0) break;
     const int rows = y.kind[kk].rows, cols = y.kind[kk].cols;
     const long first = m->off(kk, d.L - 1), stride = d.L > 1 ? m->off(kk, d.L - 2) - first : (long)rows * cols;
+    int nl = 0;
     pr = prof_begin(m);
     GPT2_TRY(muon::update(m->params() + first, m->pbf() + first, m->grads() + first, m->at<float>(y.adam_m) + first,
                           stride, d.L, rows, cols, lr, momentum, m->cfg.weight_decay, &m->sc()->gscale, &m->sc()->skip,
-                          workspace, ws_bytes, m->err(), m->stream));
-    prof_end(m, pr, PC_OPT, 30.0 * (double)d.L * rows * cols, muon::kUpdateLaunches);
+                          workspace, ws_bytes, m->err(), m->stream, &nl));
+    prof_end(m, pr, PC_OPT, 30.0 * (double)d.L * rows * cols, nl);
   }
   return grad_norm_out ? read_grad_norm(m, grad_norm_out) : GPT2_OK;
 }
@@ -1703,15 +1704,12 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
   a.losses = losses; a.coef = reinterpret_cast<float*>(stats + N); a.N = N; a.V = V; a.ignore_index = ignore_index;
   a.err = dev_err;
   GPT2_TRY(pt::pair_losses(a, P, s));
-  if (dlogits) {
-    pt::PairGradArgs g{};
-    g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats; g.coef = a.coef;
-    g.dlogits = static_cast<bf16*>(dlogits);
-    g.n_seq = 2 * P; g.V = V; g.Vp = Vp; g.ignore_index = ignore_index;
-    g.N = N;
-    return pt::pair_gradients(g, s);
-  }
-  return GPT2_OK;
+  if (!dlogits) return GPT2_OK;
+  pt::PairGradArgs g{};
+  g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats; g.coef = a.coef;
+  g.dlogits = static_cast<bf16*>(dlogits);
+  g.N = N; g.n_seq = 2 * P; g.V = V; g.Vp = Vp; g.ignore_index = ignore_index;
+  return pt::pair_gradients(g, s);
 }
 
 size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols) {

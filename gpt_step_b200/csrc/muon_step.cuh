@@ -8,14 +8,18 @@ namespace muon {
 
 // out[b] = the orthogonalised x[b], bf16 [rows][cols]; matrices x_stride, out_stride
 // elements apart. have_parts: the workspace holds the partial sums of squares.
+// *launches (may be null) grows by the kernels launched.
 template <typename T>
 int orthogonalize(const T* x, long x_stride, bf16* out, long out_stride, int batch, int rows, int cols, int steps,
-                  void* ws, size_t ws_bytes, int* err, cudaStream_t s, bool have_parts = false) {
+                  void* ws, size_t ws_bytes, int* err, cudaStream_t s, bool have_parts = false,
+                  int* launches = nullptr) {
   Work w;
   if (!plan(batch, rows, cols, &w) || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255))
     return GPT2_ERR_ARG;
   if (steps < 1 || steps > kMaxSteps) return GPT2_ERR_ARG;
-  if (small::fits(w.n, w.m))
+  const bool on_chip = small::fits(w.n, w.m);
+  if (launches) *launches += on_chip ? 1 : have_parts ? 2 : 3;
+  if (on_chip)
     return small::run(x, x_stride, out, out_stride, batch, rows, cols, steps, err, s);
   char* base = static_cast<char*>(ws);
   if (prepare_x(w, base, x, x_stride, batch, rows, cols, have_parts, s) != cudaSuccess) return GPT2_ERR_CUDA;
@@ -88,8 +92,6 @@ __global__ void __launch_bounds__(256) apply_kernel(float* __restrict__ w, bf16*
   }
 }
 
-constexpr int kUpdateLaunches = 4;   // momentum, convert, the rounds, apply
-
 // Muon's update of a batch of fp32 weights (matrices `stride` elements apart,
 // rows * cols a multiple of 4): the orthogonalised momentum scaled to the
 // root-mean-square of an AdamW step, 0.2 sqrt(max(rows, cols)).
@@ -101,7 +103,7 @@ inline size_t update_workspace(int batch, int rows, int cols) {
 
 inline int update(float* w, bf16* wb, float* g, float* mom, long stride, int batch, int rows, int cols, float lr,
                   float mu, float wd, const float* gscale, const int* skip, void* ws, size_t ws_bytes, int* err,
-                  cudaStream_t s) {
+                  cudaStream_t s, int* launches) {
   Work wk;
   if (!plan(batch, rows, cols, &wk) || ws_bytes < update_workspace(batch, rows, cols)) return GPT2_ERR_ARG;
   const long count = (long)rows * cols;
@@ -111,7 +113,8 @@ inline int update(float* w, bf16* wb, float* g, float* mom, long stride, int bat
   if (launch_pdl(momentum_kernel, dim3(wk.parts, batch), dim3(256), 0, s, g, mom, stride, count / 4, mu, gscale, skip,
                  reinterpret_cast<double*>(base + wk.part)) != cudaSuccess)
     return GPT2_ERR_CUDA;
-  const int st = orthogonalize<float>(g, stride, o, count, batch, rows, cols, 5, ws, wk.total, err, s, true);
+  const int st = orthogonalize<float>(g, stride, o, count, batch, rows, cols, 5, ws, wk.total, err, s, true, launches);
+  *launches += 2;
   if (st != GPT2_OK) return st;
   const float adj = 0.2f * sqrtf((float)std::max(rows, cols));
   return launch_pdl(apply_kernel, dim3(wk.parts, batch), dim3(256), 0, s, w, wb, g, (const bf16*)o, stride, count / 4,

@@ -569,12 +569,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   const int p = blockIdx.x;
   bool bad = false;
   for (int h = 0; h < 2; ++h) {
-    int b, e;
+    long b, e;
     if (a.seq_start) {
       b = a.seq_start[2 * p + h];
       e = a.seq_start[2 * p + h + 1];
     } else {
-      b = (2 * p + h) * a.seq_len;
+      b = (2L * p + h) * a.seq_len;
       e = b + a.seq_len;
     }
     if (b < 0 || e < b || e > a.N) {
@@ -584,9 +584,9 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
     double s = 0.0;
     int n = 0;
 #pragma unroll 4
-    for (int i = b + threadIdx.x; i < e; i += kPairThreads) s += (double)a.logps[i];   // 0 for rows left out
+    for (long i = b + threadIdx.x; i < e; i += kPairThreads) s += (double)a.logps[i];   // 0 for rows left out
     if (a.average)
-      for (int i = b + threadIdx.x; i < e; i += kPairThreads) n += row_kept(a.targets[i], a.V, a.ignore_index);
+      for (long i = b + threadIdx.x; i < e; i += kPairThreads) n += row_kept(a.targets[i], a.V, a.ignore_index);
     s = warp_sum_d(s);
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane_id() == 0) {

@@ -416,6 +416,72 @@ def test_operators_on_another_stream_and_in_a_graph():
     assert not np.array_equal(replayed[0], first[0]) and not np.array_equal(replayed[-1], first[-1])
 
 
+@pytest.mark.parametrize("b,r,c", [(3, 333, 517), (1, 700, 300), (4, 100, 900)])
+def test_orthogonalize_captured_replayed_and_twice_at_once(b, r, c):
+    """Every launch form in a graph, and two calls at a time on two streams with workspaces of their own."""
+    rng = np.random.default_rng(b * r + c)
+    xs = [f32(rng.standard_normal((b, r, c))) for _ in range(2)]
+    ref = [run_ns(x) for x in xs]
+    outs = [torch.zeros(b, r, c, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    wss = [torch.empty(gs.orthogonalize_workspace(b, r, c), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    err = err_word()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            gs.orthogonalize(xs[i], outs[i], wss[i], err, stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(np.array_equal(host(outs[i]), ref[i]) for i in range(2)) and int(err.sum()) == 0
+    buf = xs[0].clone()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:                                        # two graphs on one workspace, replayed in order
+        with torch.cuda.graph(g):
+            gs.orthogonalize(buf, outs[0], wss[0], err)
+    outs[0].zero_()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(host(outs[0]), ref[0])
+    buf.copy_(xs[1])
+    graphs[1].replay()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(host(outs[0]), ref[1]) and int(err.sum()) == 0
+
+
+@pytest.mark.parametrize("V,Vp,T", [(1000, 1024, 37), (4353, 4480, 148), (9001, 9008, 64)])
+def test_policy_loss_over_more_rows_than_stay_resident(V, Vp, T):
+    """Rows in windows, most of them left out, the last window short: every row is written once."""
+    N = 9000 if V < 4000 else 6000
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(N, Vp, device="cuda", generator=gen).to(torch.bfloat16)
+    t = torch.randint(0, V, (N,), device="cuda", generator=gen)
+    t[torch.arange(N, device="cuda") % T < int(0.7 * T)] = -1
+    t = t.to(torch.int32)
+    lp = torch.log_softmax(z[:, :V].double(), 1).gather(1, t.clamp(min=0).long()[:, None])[:, 0]
+    old = (lp - 0.1).float()
+    dz, logps, losses = torch.full_like(z, 3.0), torch.full((N,), 5.0, device="cuda"), torch.full((N,), 5.0, device="cuda")
+    err = err_word()
+    gs.policy_loss(z, t, old, torch.ones(N, device="cuda"), dz, logps, losses, V, err)
+    keep = t >= 0
+    want = torch.where(keep, lp, 0.0).cpu().numpy()
+    assert np.all(np.abs(host(logps) - want) <= np.where(keep.cpu().numpy(), lp_tol(want), 0.0))
+    g = torch.where(keep, -torch.exp(lp - old.double()), 0.0)
+    ref = -g[:, None] * torch.softmax(z[:, :V].double(), 1)
+    ref[torch.arange(N, device="cuda"), t.clamp(min=0).long()] += g
+    off = (dz[:, :V].double() - ref).abs()
+    tol = 2.0 ** -8 * ref.abs() * (1 + 2.0 ** -6) + 2.0 ** -17 * g.abs()[:, None] + 1e-38
+    assert bool((off <= tol).all()) and bool((dz[:, V:] == 0).all()) and bool((dz[~keep] == 0).all())
+    assert int(err.sum()) == 0
+    seq = torch.tensor([0, 11, N - 1500, N - 700, N - 3], dtype=torch.int32, device="cuda")
+    out2 = torch.full((N,), 5.0, device="cuda")
+    ws = torch.empty(gs.preference_loss_workspace(N, 2), dtype=torch.uint8, device="cuda")
+    dz2 = torch.full_like(z, 3.0)
+    gs.preference_loss(z, t, seq, dz2, out2, None, torch.empty(2, device="cuda"), V, ws, err)
+    assert torch.equal(out2[:N - 3], logps[:N - 3]) and bool((out2[N - 3:] == 5.0).all())
+    assert bool((dz2[N - 3:] == 3.0).all()) and bool((dz2[:N - 3][~keep[:N - 3]] == 0).all())
+    assert bool((dz2[:N - 3][keep[:N - 3]][:, :V] != 3.0).all())
+
+
 # -- the model calls ---------------------------------------------------------------------------
 
 # bars of the whole step for bf16 activations, as in test_gpu_model.py

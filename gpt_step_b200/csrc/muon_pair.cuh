@@ -9,12 +9,24 @@
 // their fills and drains are one. The wait ends: every tile waits only for earlier
 // ones, every pair works in order, and the launch is cooperative, so all are resident.
 //
-// Inside a pair: a TMA warp, an issuing warp and eight epilogue warps; two
-// accumulators in tensor memory, so that a tile's epilogue runs under the next tile's
-// main loop. A and P are symmetric: only tiles that touch or lie below the diagonal are
-// computed, and a chunk below it is staged a second time turned over and stored to its
-// mirror image. The a I of P stands in P's fp16 values: rounding P near 0.7 costs less
-// than rounding Q = P - a I near -2.8, and the last product then reads nothing but lo.
+// Inside a pair: a TMA warp, an issuing warp, a warp that looks whether the next tiles'
+// inputs are finished, and eight epilogue warps; two accumulators in tensor memory, so that
+// a tile's epilogue runs under the next tile's main loop. A and P are symmetric: only tiles
+// that touch or lie below the diagonal are computed, and a chunk below it is staged a second
+// time turned over and stored to its mirror image. The a I of P stands in P's fp16 values:
+// rounding P near 0.7 costs less than rounding P - a I near -2.8, and the last product then
+// reads nothing but lo.
+//
+// What bounds it: large matrices the tensor pipe under the power limit (16 x 1,536 x 6,144:
+// 4.10 ms, 0.92 PFLOP/s of the products with symmetric ones counted half); 768 rows the
+// shared memory, whose bandwidth the operands take whole at the full tensor rate (64 bytes a
+// clock in and out) and an APPLY tile's hi, lo and aux boxes half as much again (tile 6.4 us
+// against 4.5 of main loop; 12 x 2,304 x 768: 470 us, tensor pipe 41% busy); small ones the
+// latency of a product, 5.5 to 7.5 us: loads and MMA 1.8, epilogue 2, its stores in memory
+// and seen by the next product 1.5 (3 x 333 x 517: 125 us). Measured and rejected: results
+// by 16-byte stores out of the boxes (3 x 333 x 517 145 us, 12 x 2,304 x 768 500 us), by
+// 32-byte stores of a row a lane (144, 575), sixteen epilogue warps with a box each (139,
+// 483); three launches a round (146 us and, with the same preparation, about 440).
 #pragma once
 #include "gemm2sm.cuh"
 #include "muon.cuh"

@@ -2,20 +2,20 @@
 // launch: a matrix stays on chip from its first read to the result.
 //
 // A cluster of nc CTAs takes one matrix X [n <= 128 rows, m columns]; each holds
-// w = 64 ceil(m / (64 nc)) <= 256 columns (384 where it is alone) in shared memory
-// as hi and lo fp16. The
-// columns stand in blocks of 64: a block is 128 rows of 128 bytes in the 128-byte
-// swizzle, which is the K-major tile of X that X X^T wants and, read the other way,
-// the MN-major tile that P X wants. A round is three products with their
-// accumulators in tensor memory (128 x 128 twice, 128 x w) and three passes of
-// registers between tensor and shared memory. Only X X^T needs the other CTAs: each
-// sends its partial sum's columns to the CTA that adds them up (fp32, in the order
-// of the ranks), which sends the sum to all as fp16. Every CTA
-// forms A A and P for itself.
+// w = 64 ceil(m / (64 nc)) <= 256 columns (384 where it is alone) in shared memory as
+// hi and lo fp16. The columns stand in blocks of 64: a block is 128 rows of 128 bytes in
+// the 128-byte swizzle, which is the K-major tile of X that X X^T wants and, read the
+// other way, the MN-major tile that P X wants. A round is three products with their
+// accumulators in tensor memory (128 x 128 twice, 128 x w) and three passes of registers
+// between tensor and shared memory. Only X X^T needs the other CTAs: each sends its partial
+// sum's columns to the CTA that adds them up (fp32, in the order of the ranks), which sends
+// the sum to all as fp16. Every CTA forms A A and P for itself.
 //
-// What bounds it is latency: about 15 dependent steps of 1 us. As separate launches
-// (two passes over M, then three products a round) the same work took 104 us for one
-// 128 x 128 matrix, 6 us a launch.
+// What bounds it is latency: 15 dependent steps. On the device a CTA alone takes 3.1 us a
+// round at 128 columns, 4.4 at 256, 5.7 at 384; a cluster of eight at 2,048 columns 10 us.
+// 1 x 128 x 128: 22 us (as separate launches, two passes over M and three products a round,
+// 104 us); 1 x 128 x 2,048: 60 us; 16 of them 122 us. A result stored one bf16 a thread, its
+// own row each, took 20 us more than rows out of shared memory.
 #pragma once
 #include "gemm2sm.cuh"
 #include "muon.cuh"

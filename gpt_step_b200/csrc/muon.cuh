@@ -2,7 +2,7 @@
 //
 // For each matrix M of a batch, X = M / (|M|_F + 1e-7), taken with the smaller
 // dimension as its n rows (m columns), goes through `steps` rounds of
-//   A = X X^T,   Q = b A + c A A,   X <- a X + Q X,
+//   A = X X^T,   P = a I + b A + c A A,   X <- P X,
 // (a, b, c) = (3.4445, -4.7750, 2.0315): every singular value s becomes
 // a s + b s^3 + c s^5, which takes any s in (0, 1] to about 0.7 .. 1.2 in five
 // rounds and leaves the singular vectors as they are.
@@ -11,10 +11,10 @@
 // rounding error that lies along them. With bf16 operands the result is 1% (a
 // flat spectrum) to 4% (a falling one) off; fp16 operands have three more bits
 // at the same tensor rate and their range is enough, because every element of X,
-// A, Q is bounded (1.21, 1.46, 12): they are held times 2^10. The term a X, along
-// which the growth happens, is added in fp32 from X held as two fp16 numbers
-// (hi + lo, 22 bits) in all but the last two rounds; the tensor cores see hi
-// alone. That ends 0.1% off for either spectrum (0.5% without lo) for no more
+// A, P is bounded (1.21, 1.46, 16): they are held times 2^10. X is held as two fp16
+// numbers (hi + lo, 22 bits) in all but the last two rounds: the tensor cores see hi
+// alone, and a lo, its part in the term a X along which the growth happens, is added
+// in fp32. That ends 0.1% off for either spectrum (0.5% without lo) for no more
 // matrix instructions, below the 0.17% of the bf16 result's own rounding.
 #pragma once
 #include <cuda_fp16.h>

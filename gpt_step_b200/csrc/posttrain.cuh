@@ -73,7 +73,7 @@ GPT2_DEV void chunk_exp(uint4 u, float c, float2 (&e)[4]) {
 // Two values rounded to bf16 on the fp32 pipe: x (2^16 + 1) - (x (2^16 + 1) - x) is x
 // rounded to 8 bits (Dekker's splitting), its upper half the bf16. The conversion
 // instruction shares the pipe of ex2, which is what bounds these kernels next to memory.
-// A value past 2^111 or a NaN becomes NaN, as its gradient row would be of no use.
+// For values below 2^111.
 GPT2_DEV uint32_t round_bf16x2(float2 x) {
   const float2 c = f2_mul(x, make_float2(65537.f, 65537.f));
   const float2 d = f2_fma(x, make_float2(-1.f, -1.f), c);
@@ -81,20 +81,32 @@ GPT2_DEV uint32_t round_bf16x2(float2 x) {
   return __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x7632);
 }
 
-// A chunk of the gradient g ([j == t] - 2^(y - c) / S), gs = -g / S; 0 behind the real columns.
-GPT2_DEV void store_chunk(uint4* dst, uint4 z, int col0, int t, int V, float c, float gs, float g) {
-  float2 e[4];
-  chunk_exp(z, c, e);
+// A row's gradient g ([j == t] - 2^(y - c) / S), 0 behind the real columns, by chunks.
+struct RowGradient {
+  int V, t, t_chunk, edge;       // edge: the chunk with the last real column and padded ones, or -1
+  float c, g, gs;
+
+  GPT2_DEV RowGradient(int V_, int t_, float c_, float s, float g_)
+      : V(V_), t(t_), t_chunk(t_ >> 3), edge((V_ & 7) ? V_ >> 3 : -1), c(c_), g(g_), gs(-g_ / s) {}
+  // Whether no value (none exceeds |g|) leaves the range of round_bf16x2.
+  GPT2_DEV bool rounds() const { return fabsf(g) < 1e30f; }
+
+  template <bool ROUNDS>
+  GPT2_DEV void store(uint4* dst, uint4 z, int i) const {
+    float2 e[4];
+    chunk_exp(z, c, e);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) e[j] = f2_mul(e[j], make_float2(gs, gs));
-  if (col0 + 8 > V || (unsigned)(t - col0) < 8u) {
-    // the target's chunk, and the last one, whose padded columns get exactly 0
-    float* f = &e[0].x;
+    for (int j = 0; j < 4; ++j) e[j] = f2_mul(e[j], make_float2(gs, gs));
+    if (i == t_chunk || i == edge) {
+      float* f = &e[0].x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = col0 + j >= V ? 0.f : f[j] + (col0 + j == t ? g : 0.f);
+      for (int j = 0; j < 8; ++j) f[j] = i * 8 + j >= V ? 0.f : f[j] + (i * 8 + j == t ? g : 0.f);
+    }
+    __stcs(dst + i, ROUNDS ? make_uint4(round_bf16x2(e[0]), round_bf16x2(e[1]), round_bf16x2(e[2]), round_bf16x2(e[3]))
+                           : make_uint4(pack_bf16x2(e[0].x, e[0].y), pack_bf16x2(e[1].x, e[1].y),
+                                        pack_bf16x2(e[2].x, e[2].y), pack_bf16x2(e[3].x, e[3].y)));
   }
-  __stcs(dst, make_uint4(round_bf16x2(e[0]), round_bf16x2(e[1]), round_bf16x2(e[2]), round_bf16x2(e[3])));
-}
+};
 
 // Columns from c0 on (a multiple of 8) of a gradient row, 0.
 GPT2_DEV void zero_row(uint4* dst, int c0, int Vp, int lane, int lanes) {
@@ -143,8 +155,13 @@ GPT2_DEV void streamed_stats(const uint4* zr, int V, float& c, float& s) {
 GPT2_DEV void streamed_gradient(const uint4* zr, uint4* dst, int t, int V, int Vp, float c, float s, float g, int lane,
                                 int lanes) {
   constexpr int kUnroll = 4;
-  const float gs = -g / s;
+  const RowGradient grad(V, t, c, s, g);
   const int nvr = (V + 7) / 8;
+  if (!grad.rounds()) {
+    for (int i = lane; i < nvr; i += lanes) grad.store<false>(dst, __ldcs(zr + i), i);
+    zero_row(dst, nvr * 8, Vp, lane, lanes);
+    return;
+  }
   for (int i0 = lane; i0 < nvr; i0 += lanes * kUnroll) {
     uint4 u[kUnroll];
 #pragma unroll
@@ -155,7 +172,7 @@ GPT2_DEV void streamed_gradient(const uint4* zr, uint4* dst, int t, int V, int V
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) {
       const int i = i0 + q * lanes;
-      if (i < nvr) store_chunk(dst + i, u[q], i * 8, t, V, c, gs, g);
+      if (i < nvr) grad.store<true>(dst, u[q], i);
     }
   }
   zero_row(dst, nvr * 8, Vp, lane, lanes);
@@ -268,7 +285,10 @@ struct RowWindows {
 // works on it, so a slot takes the next row's chunk as soon as this row is done with it,
 // without a barrier, and copies run under the arithmetic and the stores. The sum takes the
 // target's logit as its reference, c = y_t, which needs no pass for the maximum; a row
-// where that overflows is summed again from its maximum.
+// whose sum passes kSumMax (a log-probability below -41) is summed again from its maximum,
+// long before the sum, or the gradient's factor g / S, leaves the range of fp32.
+constexpr float kSumMax = 1e18f;
+
 template <int G>
 struct RowPipe {
   static constexpr int kThreads = 32 * G;
@@ -386,7 +406,7 @@ __global__ void __launch_bounds__(32 * G, 32 / G) policy_loss_kernel(const Polic
     const float zt = cur.zt;
     pipe.arrive(a.V);
     float c = zt * k::kLog2eF, s = pipe.sum_from(c, nullptr);
-    if (!(s < 3e38f)) {   // (the same in every thread)
+    if (!(s < kSumMax)) {   // (the same in every thread)
       __nv_bfloat162 m2 = as_bf2(kNegInf2);
       for (int i = threadIdx.x; i < pipe.nvr; i += 32 * G) m2 = __hmax2(m2, chunk_max(row_slots[i]));
       const float2 mf = __bfloat1622float2(m2);
@@ -411,23 +431,25 @@ __global__ void __launch_bounds__(32 * G, 32 / G) policy_loss_kernel(const Polic
     uint4* dr = a.dlogits ? reinterpret_cast<uint4*>(a.dlogits + off) : nullptr;
     const uint4* zn = j >= 0 ? reinterpret_cast<const uint4*>(a.logits + (size_t)cur.row * a.Vp) : nullptr;
     const bool none = !dr || (g == 0.f && isfinite(lp));
-    const float gs = -g / s;
     if (none) {
+      if (zn) pipe.prefetch(zn);
+    } else if (const RowGradient grad(a.V, t, c, s, g); !grad.rounds()) {
+      for (int i = threadIdx.x; i < pipe.nvr; i += 32 * G) grad.template store<false>(dr, row_slots[i], i);
       if (zn) pipe.prefetch(zn);
     } else {
       constexpr int kT = 32 * G;
       int i = threadIdx.x;
       for (; i + kT < pipe.nvr; i += 2 * kT) {   // two chunks in flight
         const uint4 u0 = row_slots[i], u1 = row_slots[i + kT];
-        store_chunk(dr + i, u0, i * 8, t, a.V, c, gs, g);
-        store_chunk(dr + i + kT, u1, (i + kT) * 8, t, a.V, c, gs, g);
+        grad.template store<true>(dr, u0, i);
+        grad.template store<true>(dr, u1, i + kT);
         if (zn) {
           cp_async16(pipe.slot0 + i * 16, zn + i);
           cp_async16(pipe.slot0 + (i + kT) * 16, zn + i + kT);
         }
       }
       if (i < pipe.nvr) {
-        store_chunk(dr + i, row_slots[i], i * 8, t, a.V, c, gs, g);
+        grad.template store<true>(dr, row_slots[i], i);
         if (zn) cp_async16(pipe.slot0 + i * 16, zn + i);
       }
     }
@@ -516,7 +538,7 @@ __global__ void __launch_bounds__(32 * G, 32 / G) row_logp_kernel(const RowArgs 
     const uint4* zn = j >= 0 ? reinterpret_cast<const uint4*>(a.logits + (size_t)next * a.Vp) : nullptr;
     pipe.arrive(a.V);
     float c = zt * k::kLog2eF, s = pipe.sum_from(c, zn);
-    if (!(s < 3e38f))   // (the same in every thread) the slots have moved on
+    if (!(s < kSumMax))   // (the same in every thread) the slots have moved on
       streamed_stats<G>(reinterpret_cast<const uint4*>(a.logits + (size_t)row * a.Vp), a.V, c, s);
     if (threadIdx.x == 0) {
       a.logps[row] = row_logp(zt, c, s);

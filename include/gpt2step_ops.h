@@ -239,7 +239,9 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
  * (3.4445, -4.7750, 2.0315): the singular values go to about 0.7 .. 1.2, the
  * singular vectors stay. Operands are fp16 with fp32 sums; five steps end about
  * 1e-3 (relative, Frobenius) from the 64-bit result before the rounding of out.
- * A zero matrix gives zeros; an infinity or NaN gives NaN in its own matrix.
+ * A zero matrix gives zeros; an infinity or NaN gives NaN in its own matrix. For
+ * |x|_F below 1e-10, where the 1e-7 leaves next to nothing of X, the result is
+ * small but loses accuracy to fp16's range.
  * out must not overlap x. The workspace is 256-byte aligned; concurrent calls
  * must not share one. */
 size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols);

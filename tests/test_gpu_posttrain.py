@@ -143,26 +143,45 @@ def test_rows_without_a_finite_log_probability_stay_in_their_rows(V, Vp):
 def test_targets_far_below_the_largest_logit(V, Vp):
     """Differences past the exponents of fp32, both ways: log-probabilities and gradients stay finite."""
     rng = np.random.default_rng(V)
-    z = rounded(rng.standard_normal((6, Vp)))
-    t = np.array([3, 5, 7, V - 1, 11, 13])
+    z = rounded(rng.standard_normal((12, Vp)))
+    t = np.array([3, 5, 7, V - 1, 11, 13, 15, 17, 19, 21, 23, 25])
     z[0, 4] = z[1, 6] = 400.0                              # the target 400 below another id
     z[2, 7] = 400.0                                        # and above all
     z[3, :V] -= 30000.0
     z[4, :V] += 30000.0
-    old = np.zeros(6)
+    for row, up in zip(range(6, 12), (20.0, 40.0, 60.0, 80.0, 86.0, 90.0)):
+        z[row, 4] = up                                      # around the exponents' end, and well before it
     z = rounded(z)
     lp, p, keep = PT.token_logps(z, t, V)
-    old = np.where(lp < -80, lp, 0.0)
-    rl, rlp, rdz = PT.policy_loss(z, t, V, old.astype(np.float32), np.ones(6), clip_high=0.5)
-    losses, logps, err = torch.empty(6, device="cuda"), torch.empty(6, device="cuda"), err_word()
-    dz = torch.empty(6, Vp, dtype=torch.bfloat16, device="cuda")
-    gs.policy_loss(bf16(z), i32(t), f32(old), f32(np.ones(6)), dz, logps, losses, V, err, clip_high=0.5)
+    old = np.where(lp < -15, lp, 0.0)
+    ds = 1e-7
+    rl, rlp, rdz = PT.policy_loss(z, t, V, old.astype(np.float32), np.ones(12), clip_high=0.5, dscale=ds)
+    losses, logps, err = torch.empty(12, device="cuda"), torch.empty(12, device="cuda"), err_word()
+    dz = torch.empty(12, Vp, dtype=torch.bfloat16, device="cuda")
+    gs.policy_loss(bf16(z), i32(t), f32(old), f32(np.ones(12)), dz, logps, losses, V, err, clip_high=0.5, dscale=ds)
     # the logits themselves are large here: y - c is one rounding of a difference, its factor log2(e) 2^-25
     tol = 2.0 ** -19 + 2.0 ** -22 * np.abs(rlp)
     assert np.all(np.abs(host(logps) - rlp) <= tol)
-    g = np.abs(np.exp(np.minimum(rlp - old, 1.0)))
-    assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g) + (tol * g)[:, None])
+    g = np.abs(np.exp(np.minimum(rlp - old, 1.0))) * ds
+    # the ratio's error: lp's, and old's rounding to fp32 (2^-24 of it)
+    rough = tol + 2.0 ** -24 * np.abs(old)
+    assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g) + rough[:, None] * np.abs(rdz) + (rough * g)[:, None])
+    # elements far from the target's are exact to their rounding: p must not fall to 0
+    assert np.all((host(dz)[:, 4] != 0) == (np.abs(rdz[:, 4]) > 1e-37))
     assert int(err.sum()) == 0
+
+
+def test_policy_loss_of_enormous_advantages():
+    """Gradients up to the end of bf16's range are finite values."""
+    rng, z, t = rows_case(6, 300, 304, 4, masked=0.0)
+    lp, _, _ = PT.token_logps(z, t, 300)
+    adv = np.array([1e30, 1e33, -1e36, 1e38, 3.0, -1e31])
+    rl, rlp, rdz = PT.policy_loss(z, t, 300, lp.astype(np.float32), adv)
+    losses, dz, err = torch.empty(6, device="cuda"), torch.empty(6, 304, dtype=torch.bfloat16, device="cuda"), err_word()
+    gs.policy_loss(bf16(z), i32(t), f32(lp), f32(adv), dz, None, losses, 300, err)
+    got = host(dz)
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - rdz) <= grad_tol(rdz, np.abs(adv) * 1.1))
 
 
 def ragged(rng, S, most, gap=True):

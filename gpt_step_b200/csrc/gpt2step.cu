@@ -565,23 +565,21 @@ int spec_loss(gpt2_model* m, const LossSpec& spec, const int32_t* tgt, int N, bf
     r.targets = tgt; r.part = lse_part; r.tgt_val = tgt_val; r.slots = slots; r.V = d.V; r.Vp = d.Vp;
     r.ignore_index = spec.ignore_index; r.err = m->err(); r.N = N;
     r.logps = spec.kind == LossSpec::LOGPS ? spec.logps : losses;
-    // the row and pair scratch lives in the attention backward's per-query terms,
-    // which are free until that runs (32 bytes a row and head)
+    // the scratch lives in the attention backward's per-query terms, which are free
+    // until that runs (32 bytes a row and head): (c, S) of the rows, coefficients and losses of the pairs
     const int P = d.B / 2;
     float2* stats = m->at<float2>(y.attD);
-    float* coef = reinterpret_cast<float*>(stats + d.N);
     if (spec.kind == LossSpec::PREFERENCE) r.stats = stats;
     GPT2_TRY(pt::row_logps(r, s));
     if (spec.kind == LossSpec::PREFERENCE) {
       pt::PairArgs a = spec.pair;
       a.logps = losses; a.targets = tgt; a.seq_start = nullptr; a.seq_len = d.T; a.N = N; a.V = d.V;
-      a.ignore_index = spec.ignore_index; a.coef = coef; a.losses = coef + 2 * P; a.err = m->err();
-      GPT2_TRY(pt::pair_losses(a, P, s));
+      a.ignore_index = spec.ignore_index; a.losses = reinterpret_cast<float*>(stats + d.N + P); a.err = m->err();
       pt::PairGradArgs g{};
       g.logits = g.dlogits = logits;
-      g.targets = tgt; g.stats = stats; g.coef = coef; g.n_seq = 2 * P; g.seq_len = d.T; g.V = d.V; g.Vp = d.Vp;
+      g.targets = tgt; g.stats = stats; g.n_seq = 2 * P; g.seq_len = d.T; g.V = d.V; g.Vp = d.Vp;
       g.ignore_index = spec.ignore_index; g.N = N;
-      GPT2_TRY(pt::pair_gradients(g, s));
+      GPT2_TRY(pt::pairs(g, a, stats + d.N, s));
       nl += 2;
       n_loss = P;
       loss_src = a.losses;
@@ -1701,15 +1699,12 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
   r.ignore_index = ignore_index; r.err = dev_err; r.N = N;
   GPT2_TRY(pt::row_logps(r, s));
   a.logps = logps; a.targets = targets; a.seq_start = seq_start; a.ref_logp = ref_logp; a.seq_logps = seq_logps;
-  a.losses = losses; a.coef = reinterpret_cast<float*>(stats + N); a.N = N; a.V = V; a.ignore_index = ignore_index;
-  a.err = dev_err;
-  GPT2_TRY(pt::pair_losses(a, P, s));
-  if (!dlogits) return GPT2_OK;
+  a.losses = losses; a.N = N; a.V = V; a.ignore_index = ignore_index; a.err = dev_err;
   pt::PairGradArgs g{};
-  g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats; g.coef = a.coef;
+  g.logits = r.logits; g.targets = targets; g.seq_start = seq_start; g.stats = stats;
   g.dlogits = static_cast<bf16*>(dlogits);
   g.N = N; g.n_seq = 2 * P; g.V = V; g.Vp = Vp; g.ignore_index = ignore_index;
-  return pt::pair_gradients(g, s);
+  return pt::pairs(g, a, stats + N, s);
 }
 
 size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols) {

@@ -582,7 +582,7 @@ struct PairArgs {
   const float* ref_logp;      // [2 P] or null
   float* seq_logps;           // [2 P] or null
   float* losses;              // [P]
-  float* coef;                // [2 P]: g of the sequence's kept rows
+  float2* coef;               // [P], or null where pair_grad_kernel forms them itself
   int N, seq_len, V, ignore_index, kind, average;
   float beta, smoothing, dscale;
   int* err;
@@ -595,15 +595,16 @@ struct PairArgs {
 // 57 us. One cooperative launch with grid barriers between the three steps, and groups of
 // pairs that L2 holds, measured 921 and 100 us.
 //
-// One CTA per pair. Sequence 2p is the chosen one, 2p + 1 the rejected one. The
-// sums over a sequence and the difference of the two run in 64 bits: a margin
-// of a few units is left of sums of thousands.
-__global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
-  pdl_begin();
-  constexpr int W = kPairThreads / 32;
+// The coefficients g of pair p's two sequences, 2p the chosen one and 2p + 1 the rejected
+// one, by a CTA of T threads (the same in all of them); with `put` the pair's loss and its
+// sequences' log-probabilities are written too. The sums over a sequence and the difference
+// of the two run in 64 bits: a margin of a few units is left of sums of thousands.
+template <int T>
+GPT2_DEV float2 pair_of(const PairArgs& a, int p, bool put) {
+  constexpr int W = T / 32;
   __shared__ double red[2][W];
   __shared__ int cnt[2][W];
-  const int p = blockIdx.x;
+  __shared__ float2 coef;
   bool bad = false;
   for (int h = 0; h < 2; ++h) {
     long b, e;
@@ -620,10 +621,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
     }
     double s = 0.0;
     int n = 0;
-#pragma unroll 4
-    for (long i = b + threadIdx.x; i < e; i += kPairThreads) s += (double)a.logps[i];   // 0 for rows left out
+#pragma unroll 8
+    for (long i = b + threadIdx.x; i < e; i += T) s += (double)a.logps[i];   // 0 for rows left out
     if (a.average)
-      for (long i = b + threadIdx.x; i < e; i += kPairThreads) n += row_kept(a.targets[i], a.V, a.ignore_index);
+      for (long i = b + threadIdx.x; i < e; i += T) n += row_kept(a.targets[i], a.V, a.ignore_index);
     s = warp_sum_d(s);
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane_id() == 0) {
@@ -632,40 +633,52 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
     }
   }
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  double gap[2], share[2];
-  for (int h = 0; h < 2; ++h) {
-    double s = 0.0;
-    int n = 0;
-    for (int w = 0; w < W; ++w) {
-      s += red[h][w];
-      n += cnt[h][w];
+  if (threadIdx.x == 0) {
+    double gap[2], share[2];
+    for (int h = 0; h < 2; ++h) {
+      double s = 0.0;
+      int n = 0;
+      for (int w = 0; w < W; ++w) {
+        s += red[h][w];
+        n += cnt[h][w];
+      }
+      share[h] = a.average ? 1.0 / (n > 0 ? n : 1) : 1.0;
+      s *= share[h];
+      if (put && a.seq_logps) a.seq_logps[2 * p + h] = (float)s;
+      gap[h] = s - (a.ref_logp ? (double)a.ref_logp[2 * p + h] : 0.0);
     }
-    share[h] = a.average ? 1.0 / (n > 0 ? n : 1) : 1.0;
-    s *= share[h];
-    if (a.seq_logps) a.seq_logps[2 * p + h] = (float)s;
-    gap[h] = s - (a.ref_logp ? (double)a.ref_logp[2 * p + h] : 0.0);
+    const double delta = gap[0] - gap[1], b = a.beta, eps = a.smoothing;
+    double loss, dd;
+    if (a.kind == 0) {
+      // softplus(+-x) and sigma(+-x) from one exponential
+      const double x = b * delta, e = exp(-fabs(x)), big = 1.0 / (1.0 + e), small = e * big;
+      const double l = put ? log1p(e) : 0.0, up = fmax(-x, 0.0) + l, down = fmax(x, 0.0) + l;   // softplus(-x), softplus(x)
+      loss = (1.0 - eps) * up + eps * down;
+      dd = -b * (x > 0 ? (1.0 - eps) * small - eps * big : (1.0 - eps) * big - eps * small);
+    } else {
+      const double off = delta - 0.5 / b;
+      loss = off * off;
+      dd = 2.0 * off;
+    }
+    if (bad) {   // bounds that are not bounds: no loss, no gradient, flagged
+      atomicOr(a.err, DEVERR_TOKEN_RANGE);
+      loss = dd = 0.0;
+    }
+    coef = make_float2((float)(dd * share[0] * a.dscale), (float)(-dd * share[1] * a.dscale));
+    if (put) {
+      a.losses[p] = (float)loss;
+      if (a.coef) a.coef[p] = coef;
+    }
   }
-  const double delta = gap[0] - gap[1], b = a.beta, eps = a.smoothing;
-  double loss, dd;
-  if (a.kind == 0) {
-    // softplus(+-x) and sigma(+-x) from one exponential
-    const double x = b * delta, e = exp(-fabs(x)), l = log1p(e), big = 1.0 / (1.0 + e), small = e * big;
-    const double up = fmax(-x, 0.0) + l, down = fmax(x, 0.0) + l;   // softplus(-x), softplus(x)
-    loss = (1.0 - eps) * up + eps * down;
-    dd = -b * (x > 0 ? (1.0 - eps) * small - eps * big : (1.0 - eps) * big - eps * small);
-  } else {
-    const double off = delta - 0.5 / b;
-    loss = off * off;
-    dd = 2.0 * off;
-  }
-  if (bad) {   // bounds that are not bounds: no loss, no gradient, flagged
-    atomicOr(a.err, DEVERR_TOKEN_RANGE);
-    loss = dd = 0.0;
-  }
-  a.losses[p] = (float)loss;
-  a.coef[2 * p] = (float)(dd * share[0] * a.dscale);
-  a.coef[2 * p + 1] = (float)(-dd * share[1] * a.dscale);
+  __syncthreads();
+  const float2 out = coef;
+  __syncthreads();   // the shared memory is free again
+  return out;
+}
+
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
+  pdl_begin();
+  pair_of<kPairThreads>(a, blockIdx.x, true);
 }
 
 struct PairGradArgs {
@@ -673,7 +686,6 @@ struct PairGradArgs {
   const int32_t* targets;
   const int32_t* seq_start;
   const float2* stats;
-  const float* coef;
   bf16* dlogits;
   int N, n_seq, seq_len, V, Vp, ignore_index;
 };
@@ -689,26 +701,58 @@ GPT2_DEV int find_sequence(const int32_t* start, int n_seq, int row) {
   return (lo > 0 && row < start[lo]) ? lo - 1 : -1;
 }
 
-// Rows' gradients from their pair's coefficient and their (c, S): a warp a row where G is
-// 1 (four a CTA), else the CTA's G warps.
-template <int G>
-__global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const PairGradArgs a) {
+// The rows' gradients from their (c, S): a warp a row where G is 1 (four a CTA), else the
+// CTA's G warps. OWN: the first n_seq / 2 CTAs take the pairs, and every other CTA adds up
+// its rows' pair for itself, a few thousand log-probabilities out of L2, instead of waiting
+// for a launch between (pa.coef otherwise holds the coefficients).
+template <int G, bool OWN>
+__global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const PairGradArgs a, const PairArgs pa) {
+  constexpr int kRows = G == 1 ? 4 : 1, T = G == 1 ? 128 : 32 * G;
+  __shared__ int pair_s[kRows];
+  __shared__ float2 coef_s[kRows];
   pdl_begin();
-  const int row = G == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const int lane = G == 1 ? lane_id() : threadIdx.x;
-  if (row >= a.N) return;
-  const int seq = a.seq_start ? find_sequence(a.seq_start, a.n_seq, row) : row / a.seq_len;
-  if (seq < 0 || seq >= a.n_seq) return;   // behind the last sequence: left as it was
+  const int P = OWN ? a.n_seq / 2 : 0;
+  if ((int)blockIdx.x < P) {
+    pair_of<T>(pa, blockIdx.x, true);
+    return;
+  }
+  const int w = G == 1 ? threadIdx.x >> 5 : 0, lane = G == 1 ? lane_id() : threadIdx.x;
+  const long row = (long)(blockIdx.x - P) * kRows + w;
+  int seq = -1, t = 0;
+  bool kept = false;
+  if (row < a.N) {
+    seq = a.seq_start ? find_sequence(a.seq_start, a.n_seq, (int)row) : (int)(row / a.seq_len);
+    if (seq >= a.n_seq) seq = -1;
+    t = a.targets[row];
+    kept = seq >= 0 && row_kept(t, a.V, a.ignore_index);
+  }
+  float2 c = make_float2(0.f, 0.f);
+  if (OWN) {
+    if (lane == 0) pair_s[w] = kept ? seq >> 1 : -1;
+    __syncthreads();
+    for (int i = 0; i < kRows; ++i) {     // uniform in the CTA
+      const int p = pair_s[i];
+      if (p < 0) continue;
+      int same = -1;
+      for (int j = 0; j < i; ++j)
+        if (pair_s[j] == p) same = j;
+      const float2 ci = same >= 0 ? coef_s[same] : pair_of<T>(pa, p, false);
+      if (threadIdx.x == 0) coef_s[i] = ci;
+      __syncthreads();
+    }
+    c = coef_s[w];
+  }
+  if (seq < 0) return;   // behind the last sequence: left as it was
   const size_t off = (size_t)row * a.Vp;
   uint4* dr = reinterpret_cast<uint4*>(a.dlogits + off);
-  const int t = a.targets[row];
-  if (!row_kept(t, a.V, a.ignore_index)) {
+  if (!kept) {
     zero_row(dr, 0, a.Vp, lane, 32 * G);
     return;
   }
+  if (!OWN) c = pa.coef[seq >> 1];
   const float2 st = a.stats[row];
-  streamed_gradient(reinterpret_cast<const uint4*>(a.logits + off), dr, t, a.V, a.Vp, st.x, st.y, a.coef[seq], lane,
-                    32 * G);
+  streamed_gradient(reinterpret_cast<const uint4*>(a.logits + off), dr, t, a.V, a.Vp, st.x, st.y, seq & 1 ? c.y : c.x,
+                    lane, 32 * G);
 }
 
 // acc += factor * rows * sum(losses), *mean_out = factor * sum(losses) (fp64 sums).
@@ -796,17 +840,29 @@ inline int row_logps(const RowArgs& a, cudaStream_t s) {
   });
 }
 
-inline int pair_losses(const PairArgs& a, int P, cudaStream_t s) {
-  return launched(launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, a));
+// What follows the rows' log-probabilities: the pairs' losses, and with a.dlogits the
+// gradients. Short rows form their pair's coefficient in the gradient's launch (2 x 64 x
+// 1,000: 11.8 us a call against 15.9 with a launch between, 3 x 201 x 8,449: 14.9 against
+// 15.7, 8 x 1,024 x 4,353: 56.2 against 56.5); a CTA with one long row a pair reads as much
+// for it (9 x 1,024 x 50,257: 828 us against 740). The bound on the rows keeps a single
+// sequence of any length from being added up by every CTA.
+inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s) {
+  const int P = a.n_seq / 2;
+  if (a.dlogits && a.Vp <= 16384 && a.N <= 32768) {
+    pa.coef = nullptr;
+    return a.Vp <= 4608
+               ? launched(launch_pdl(pair_grad_kernel<1, true>, dim3(P + (a.N + 3) / 4), dim3(128), 0, s, a, pa))
+               : launched(launch_pdl(pair_grad_kernel<4, true>, dim3(P + a.N), dim3(128), 0, s, a, pa));
+  }
+  pa.coef = coef;
+  const int st = launched(launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, pa));
+  if (st != GPT2_OK || !a.dlogits) return st;
+  return a.Vp <= 4608
+             ? launched(launch_pdl(pair_grad_kernel<1, false>, dim3((a.N + 3) / 4), dim3(128), 0, s, a, pa))
+             : launched(launch_pdl(pair_grad_kernel<8, false>, dim3(a.N), dim3(256), 0, s, a, pa));
 }
 
-inline int pair_gradients(const PairGradArgs& a, cudaStream_t s) {
-  if (a.Vp <= 4608) return launched(launch_pdl(pair_grad_kernel<1>, dim3((a.N + 3) / 4), dim3(128), 0, s, a));
-  if (a.Vp <= 16384) return launched(launch_pdl(pair_grad_kernel<4>, dim3(a.N), dim3(128), 0, s, a));
-  return launched(launch_pdl(pair_grad_kernel<8>, dim3(a.N), dim3(256), 0, s, a));
-}
-
-// Workspace: a row's (c, S), then a sequence's coefficient.
+// Workspace: the rows' (c, S), then the pairs' coefficients.
 inline size_t preference_workspace(int N, int P) { return (size_t)N * 8 + (size_t)P * 8; }
 
 }  // namespace pt

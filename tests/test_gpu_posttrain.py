@@ -243,6 +243,30 @@ def test_preference_loss(P, most, V, Vp, kind, average, smoothing, inplace):
     assert np.array_equal(got[~inside], untouched, equal_nan=True)
 
 
+def test_preference_loss_of_many_rows_and_without_a_gradient():
+    """More rows than the gradient's launch takes on the pairs as well, and losses alone."""
+    N, V, Vp, P = 33000, 40, 40, 3
+    rng, z, t = rows_case(N, V, Vp, 17)
+    start = np.array([0, 30000, 30001, 30001, 31000, 32000, 33000])
+    rl, rs, rlp, rdz = PT.preference_loss(z, t, V, start, average=True, beta=0.5, dscale=1.0)
+    out = []
+    for grad in (True, False):
+        dz = torch.full((N, Vp), 5.0, dtype=torch.bfloat16, device="cuda") if grad else None
+        logps, losses, seq, err = (torch.empty(N, device="cuda"), torch.empty(P, device="cuda"),
+                                   torch.empty(2 * P, device="cuda"), err_word())
+        ws = torch.empty(gs.preference_loss_workspace(N, P), dtype=torch.uint8, device="cuda")
+        gs.preference_loss(bf16(z), i32(t), i32(start), dz, logps, seq, losses, V, ws, err, average=True, beta=0.5)
+        assert np.max(np.abs(host(seq) - rs)) <= lp_tol(np.abs(rlp).max()) + 1e-6
+        assert np.max(np.abs(host(losses) - rl)) <= 1e-4 and int(err.sum()) == 0
+        out.append((host(losses), host(logps)))
+        if grad:
+            n = np.array([(t[start[i]:start[i + 1]] != -1).sum() for i in range(2 * P)])
+            g = np.repeat(0.5 / np.maximum(n, 1), np.diff(start))
+            # the margins' errors change the slope by less than beta^2 times them: 1e-4 of it
+            assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g) + 1e-4 * np.abs(g)[:, None])
+    assert all(np.array_equal(a, b) for a, b in zip(*out))
+
+
 def test_preference_loss_flags_bounds_that_are_not_bounds():
     rng, z, t = rows_case(20, 30, 32, 8, masked=0.0)
     for start in ([0, 5, 9, 4, 20], [0, 5, 10, 15, 21], [-3, 5, 10, 15, 20], [2000000000, 5, 10, 15, 20]):

@@ -316,11 +316,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t te0 = gemm2::mapa_shared(smem_u32(&tempty[0]), 0), te1 = gemm2::mapa_shared(smem_u32(&tempty[1]), 0);
     const bool tall = p.rows > p.cols;
     uint32_t* pending = nullptr;                    // the counter of a tile stored but not signalled
-    // What this warp stored is in memory (but for the latest `newer` groups): say so.
+    // What this warp stored is in memory (with `newer`, but for the latest group): say so.
+    // The wait makes the stores visible to this thread, the release to whoever acquires the
+    // count and, behind its proxy fence, to its loads.
     auto signal = [&](bool newer) {
       if (newer) gemm::bulk_wait_all<1>();
       else gemm::bulk_wait_all<0>();
-      asm volatile("fence.proxy.async;" ::: "memory");
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(pending) : "memory");
       pending = nullptr;
     };

@@ -578,9 +578,9 @@ def test_token_logps_of_the_model(B):
     assert math.isfinite(m.fwd_bwd(i32(x[:B]), i32(np.maximum(y[:B], 0)), want_loss=True))
 
 
-@pytest.mark.parametrize("B", [4, 2])
-def test_policy_micro_step_of_the_model(B):
-    m, ocfg = tiny(micro_batch=B)
+@pytest.mark.parametrize("B,V", [(4, 1000), (2, 1000), (4, 50257), (2, 20001)])
+def test_policy_micro_step_of_the_model(B, V):
+    m, ocfg = tiny(micro_batch=B, vocab_real=V)
     rng, x, y = tiny_batch(ocfg, 2)
     n = x.size
     p = G.init_params(ocfg, 1337)
@@ -602,9 +602,10 @@ def test_policy_micro_step_of_the_model(B):
     check_grads(ocfg, m.read_all(gs.GPT2_GRADS), oracle_grads(ocfg, p, x, dz))
 
 
-@pytest.mark.parametrize("B,kind,average", [(4, "sigmoid", False), (2, "squared", True)])
-def test_preference_micro_step_of_the_model(B, kind, average):
-    m, ocfg = tiny(micro_batch=B)
+@pytest.mark.parametrize("B,kind,average,V", [(4, "sigmoid", False, 1000), (2, "squared", True, 1000),
+                                              (4, "sigmoid", False, 50257)])
+def test_preference_micro_step_of_the_model(B, kind, average, V):
+    m, ocfg = tiny(micro_batch=B, vocab_real=V)
     rng, x, y = tiny_batch(ocfg, 3)
     p = G.init_params(ocfg, 1337)
     z = G.forward(ocfg, p, x)[2]["logits"]

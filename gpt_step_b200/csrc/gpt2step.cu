@@ -1712,11 +1712,25 @@ size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols) {
   return muon::plan(batch, rows, cols, &w) ? w.total : 0;
 }
 
+// Whether no matrix of x meets one of out: sets apart from one another, or matrices of
+// both in turn at the same distance (sizes and strides in bytes).
+static bool matrices_apart(const void* x, size_t xb, size_t xs, const void* out, size_t ob, size_t os, int batch) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+  const size_t a_all = (size_t)(batch - 1) * xs + xb, b_all = (size_t)(batch - 1) * os + ob;
+  if (b >= a + a_all || a >= b + b_all) return true;
+  if (batch == 1 || xs != os) return false;
+  const size_t d = b >= a ? (b - a) % xs : (xs - (a - b) % xs) % xs;
+  return d >= xb && d + ob <= xs;
+}
+
 int gpt2op_orthogonalize(const void* x, int x_fp32, int64_t x_stride, void* out, int64_t out_stride, int batch,
                          int rows, int cols, int steps, void* workspace, size_t ws_bytes, int* dev_err, void* stream) {
   if (!x || !out || !workspace || !dev_err) return GPT2_ERR_ARG;
   if (rows <= 0 || cols <= 0 || batch <= 0) return GPT2_ERR_ARG;
-  if (batch > 1 && (x_stride < (int64_t)rows * cols || out_stride < (int64_t)rows * cols)) return GPT2_ERR_ARG;
+  const int64_t count = (int64_t)rows * cols;
+  if (batch > 1 && (x_stride < count || out_stride < count)) return GPT2_ERR_ARG;
+  const size_t xe = x_fp32 ? 4 : 2;
+  if (!matrices_apart(x, count * xe, x_stride * xe, out, count * 2, out_stride * 2, batch)) return GPT2_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bf16* o = static_cast<bf16*>(out);
   return x_fp32 ? muon::orthogonalize(static_cast<const float*>(x), x_stride, o, out_stride, batch, rows, cols, steps,

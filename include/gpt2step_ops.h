@@ -242,7 +242,8 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
  * A zero matrix gives zeros; an infinity or NaN gives NaN in its own matrix. For
  * |x|_F below 1e-10, where the 1e-7 leaves next to nothing of X, the result is
  * small but loses accuracy to fp16's range.
- * out must not overlap x. The workspace is 256-byte aligned; concurrent calls
+ * out must not overlap x (refused; matrices of both may lie in turn, the same
+ * distance apart). The workspace is 256-byte aligned; concurrent calls
  * must not share one. */
 size_t gpt2op_orthogonalize_workspace(int batch, int rows, int cols);
 int gpt2op_orthogonalize(const void* x, int x_fp32, int64_t x_stride, void* out, int64_t out_stride, int batch,

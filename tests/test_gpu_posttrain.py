@@ -384,6 +384,17 @@ def test_orthogonalize_strided_and_unaligned_matrices():
         flat = host(out).ravel()
         for a, b in ((0, 1), (1 + 620, 778), (778 + 620, 1555), (1555 + 620, 3000)):
             assert np.all(flat[a:b] == 4.0)
+    # matrices and their results in turn in one buffer
+    buf = torch.empty(3, 20 * 31 * 3, dtype=torch.bfloat16, device="cuda")
+    x, o = buf[:, :1240].view(torch.float32).view(3, 20, 31), buf[:, 1240:].view(3, 20, 31)
+    x.copy_(torch.tensor(rng.standard_normal((3, 20, 31))))
+    given = host(x).copy()
+    gs.orthogonalize(x, o, ws, err)
+    assert np.array_equal(host(x), given)
+    for i in range(3):
+        assert rel_l2(host(o[i]), PT.newton_schulz(given[i])) <= NS_TOL
+    with pytest.raises(gs.GPT2Error):
+        gs.orthogonalize(x, buf[:, 1239:1859].as_strided((3, 20, 31), (1860, 31, 1)), ws, err)
 
 
 @pytest.mark.parametrize("b,r,c", [(12, 768, 768), (2, 2304, 768), (3, 384, 1536), (1, 1536, 6144)])

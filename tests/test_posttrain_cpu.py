@@ -133,11 +133,18 @@ def test_orthogonalize_refuses_bad_arguments(lib):
     n = ws(2, 8, 24)
     assert n > 0
 
-    def ns(x=D, xs=192, out=D, os=192, b=2, r=8, c=24, steps=5, w=D, nb=n, err=D):
+    at = ctypes.c_void_p
+    far = at(1 << 20)
+
+    def ns(x=D, xs=192, out=far, os=192, b=2, r=8, c=24, steps=5, w=D, nb=n, err=D):
         return lib.gpt2op_orthogonalize(x, 1, xs, out, os, b, r, c, steps, w, nb, err, None)
     for bad in (dict(x=None), dict(out=None), dict(w=None), dict(err=None), dict(b=0), dict(r=0), dict(c=-1),
                 dict(r=20000), dict(xs=191), dict(os=191), dict(steps=0), dict(steps=17), dict(nb=n - 1),
-                dict(w=ctypes.c_void_p(4096 + 128))):
+                dict(w=at(4096 + 128)),
+                # results over the inputs (fp32, 768 bytes a matrix): the same place, inside, across the end,
+                # from below, and between two matrices without room
+                dict(out=D), dict(out=at(4096 + 700)), dict(out=at(4096 + 1500)), dict(out=at(4096 - 600)),
+                dict(xs=256, os=512, out=at(4096 + 768))):
         assert ns(**bad) == 1, bad
 
 

@@ -591,10 +591,10 @@ struct PairArgs {
 // The preference loss reads the logits twice, in row_logp_kernel and pair_grad_kernel: no
 // row's gradient is known before all rows of its pair are. A pair of the largest case (two
 // sequences of 1,024 x 50,257) is more than L2 holds. Nine such pairs: 717 us, 4.4 TB/s of
-// the bytes needed once and 6.2 TB/s of those moved; eight pairs of up to 1,024 x 4,353:
-// 57 us. One cooperative launch with grid barriers between the three steps, and groups of
-// pairs that L2 holds, measured 921 and 100 us.
-//
+// the bytes needed once and 6.2 TB/s of those moved; eight pairs of up to 2 x 1,024 x 4,353:
+// 56 us. One cooperative launch with grid barriers between the steps, and groups of pairs
+// that L2 holds, measured 921 and 100 us.
+
 // The coefficients g of pair p's two sequences, 2p the chosen one and 2p + 1 the rejected
 // one, by a CTA of T threads (the same in all of them); with `put` the pair's loss and its
 // sequences' log-probabilities are written too. The sums over a sequence and the difference
@@ -841,25 +841,27 @@ inline int row_logps(const RowArgs& a, cudaStream_t s) {
 }
 
 // What follows the rows' log-probabilities: the pairs' losses, and with a.dlogits the
-// gradients. Short rows form their pair's coefficient in the gradient's launch (2 x 64 x
-// 1,000: 11.8 us a call against 15.9 with a launch between, 3 x 201 x 8,449: 14.9 against
-// 15.7, 8 x 1,024 x 4,353: 56.2 against 56.5); a CTA with one long row a pair reads as much
-// for it (9 x 1,024 x 50,257: 828 us against 740). The bound on the rows keeps a single
-// sequence of any length from being added up by every CTA.
+// gradients. A pair's coefficient is formed in the gradient's launch while that reads no
+// more than 4 MB (pairs of like length; the bound on the rows is for one pair that has
+// nearly all of them), a launch of its own otherwise. Pairs of 2 x 64 x 1,000 11.7 us a
+// call against 13.8, 1 of 2 x 1,024 x 1,000 15.8 against 20.2, 4 of 2 x 512 x 1,000 15.7
+// against 19.3, 16 of 2 x 128 x 1,000 13.8 either way; above, 8 of 2 x 512 x 4,353 (8 MB)
+// 45.9 against 42.1 and 1 of 2 x 8,192 x 1,000 (256 MB) 49 against 29. Rows over 16,384
+// ids take the launch: 2 of 2 x 200 x 30,000 29.0 us against 27.8.
 inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s) {
   const int P = a.n_seq / 2;
-  if (a.dlogits && a.Vp <= 16384 && a.N <= 32768) {
+  const int rows = a.Vp <= 4608 ? 4 : 1;   // a CTA's
+  if (a.dlogits && a.Vp <= 16384 && a.N <= 8192 && (long)a.N * a.N / ((long)P * rows) <= 1 << 20) {
     pa.coef = nullptr;
-    return a.Vp <= 4608
+    return rows == 4
                ? launched(launch_pdl(pair_grad_kernel<1, true>, dim3(P + (a.N + 3) / 4), dim3(128), 0, s, a, pa))
                : launched(launch_pdl(pair_grad_kernel<4, true>, dim3(P + a.N), dim3(128), 0, s, a, pa));
   }
   pa.coef = coef;
   const int st = launched(launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, pa));
   if (st != GPT2_OK || !a.dlogits) return st;
-  return a.Vp <= 4608
-             ? launched(launch_pdl(pair_grad_kernel<1, false>, dim3((a.N + 3) / 4), dim3(128), 0, s, a, pa))
-             : launched(launch_pdl(pair_grad_kernel<8, false>, dim3(a.N), dim3(256), 0, s, a, pa));
+  return rows == 4 ? launched(launch_pdl(pair_grad_kernel<1, false>, dim3((a.N + 3) / 4), dim3(128), 0, s, a, pa))
+                   : launched(launch_pdl(pair_grad_kernel<8, false>, dim3(a.N), dim3(256), 0, s, a, pa));
 }
 
 // Workspace: the rows' (c, S), then the pairs' coefficients.

@@ -22,8 +22,9 @@
 // shared memory, whose bandwidth the operands take whole at the full tensor rate (64 bytes a
 // clock in and out) and an APPLY tile's hi, lo and aux boxes half as much again (tile 6.4 us
 // against 4.5 of main loop; 12 x 2,304 x 768: 470 us, tensor pipe 41% busy); small ones the
-// latency of a product, 5.5 to 7.5 us: loads and MMA 1.8, epilogue 2, its stores in memory
-// and seen by the next product 1.5 (3 x 333 x 517: 125 us). Measured and rejected: results
+// latency of a product, 5 to 7 us: loads and MMA 1.8, epilogue 2, its stores in memory and
+// seen by the next product 1.5 (3 x 333 x 517: 116 us; 124 with a second proxy fence before a
+// finished tile's signal, when the following were measured). Measured and rejected: results
 // by 16-byte stores out of the boxes (3 x 333 x 517 145 us, 12 x 2,304 x 768 500 us), by
 // 32-byte stores of a row a lane (144, 575), sixteen epilogue warps with a box each (139,
 // 483); three launches a round (146 us and, with the same preparation, about 440).

@@ -345,7 +345,7 @@ struct RowPipe {
 };
 
 // The policy loss: a row is read from memory once and its gradient written once, which is
-// what bounds it. 19,456 x 50,257 with a quarter of the rows left out: 598 us, 5.7 TB/s of
+// what bounds it. 19,456 x 50,257 with a quarter of the rows left out: 598 to 627 us by box, 5.7 TB/s of
 // the bytes it cannot do without (0.87 of the measured copy rate); the ex2 pipe is 55% busy
 // beside it, at two exponentials an element. Measured before: the row read twice, the second
 // time out of L2, 727 us (eight CTAs an SM bring more rows than L2 holds); held in registers
@@ -590,7 +590,7 @@ struct PairArgs {
 
 // The preference loss reads the logits twice, in row_logp_kernel and pair_grad_kernel: no
 // row's gradient is known before all rows of its pair are. A pair of the largest case (two
-// sequences of 1,024 x 50,257) is more than L2 holds. Nine such pairs: 717 us, 4.4 TB/s of
+// sequences of 1,024 x 50,257) is more than L2 holds. Nine such pairs: 717 to 754 us by box, 4.4 TB/s of
 // the bytes needed once and 6.2 TB/s of those moved; eight pairs of up to 2 x 1,024 x 4,353:
 // 56 us. One cooperative launch with grid barriers between the steps, and groups of pairs
 // that L2 holds, measured 921 and 100 us.

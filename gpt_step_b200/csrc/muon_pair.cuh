@@ -18,10 +18,10 @@
 // reads nothing but lo.
 //
 // What bounds it: large matrices the tensor pipe under the power limit (16 x 1,536 x 6,144:
-// 4.10 ms, 0.92 PFLOP/s of the products with symmetric ones counted half); 768 rows the
+// 4.06 to 4.32 ms by box, 0.87 to 0.93 PFLOP/s of the products with symmetric ones counted half); 768 rows the
 // shared memory, whose bandwidth the operands take whole at the full tensor rate (64 bytes a
-// clock in and out) and an APPLY tile's hi, lo and aux boxes half as much again (tile 6.4 us
-// against 4.5 of main loop; 12 x 2,304 x 768: 470 us, tensor pipe 41% busy); small ones the
+// clock in and out) and an APPLY tile's hi, lo and aux boxes a third as much again (tile 6.4 us
+// against 4.5 of main loop when lo was fp16; 12 x 2,304 x 768: 446 us); small ones the
 // latency of a product, 5 to 7 us: loads and MMA 1.8, epilogue 2, its stores in memory and
 // seen by the next product 1.5 (3 x 333 x 517: 116 us; 124 with a second proxy fence before a
 // finished tile's signal, when the following were measured). Measured and rejected: results
@@ -52,13 +52,14 @@ enum Product : int { GRAM = 0, POLY = 1, APPLY = 2 };
 struct Maps {
   CUtensorMap a_x[2], b_x[2], c_x[2];   // X by rows of 128, by rows of BN / 2, by 64 x 64 columns
   CUtensorMap a_a, b_a, a_p;            // A by rows (both operands), P by rows
-  CUtensorMap out_x[2], out_lo, out_a, out_p, out;   // boxes of 32 x 32
+  CUtensorMap out_x[2], out_lo, out_a, out_p, out;   // boxes of 32 x 32 (lo: bytes)
 };
 
 struct Params {
   int n, m, ld_x, ld_a, batch, steps;
   int tiles_m, sym, full;               // row tiles; tiles of a symmetric product, of the last one
-  const __half *lo, *a;
+  const uint8_t* lo;                    // [batch][n][ld_x] e4m3
+  const __half* a;
   uint32_t* count;                      // [batch][3] signals of finished tiles
   bf16* result;
   long result_stride;
@@ -165,6 +166,9 @@ GPT2_DEV bool wait_ready(uint32_t at, uint32_t k, int* err) {
 
 // 16-byte chunk j of row r in a 32 x 32 box of 64-byte rows, 64-byte swizzle.
 GPT2_DEV uint32_t box_at(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
+
+// The same of a box of 32-byte rows, 32-byte swizzle.
+GPT2_DEV uint32_t lo_box_at(int r, int j) { return (uint32_t)(r * 32 + ((j ^ ((r >> 2) & 1)) << 4)); }
 
 // A lane's 32 values (its row) down a column of the box: the box turned over.
 GPT2_DEV void stage_turned(uint8_t* box, int lane, const uint32_t (&w)[16]) {
@@ -333,23 +337,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool sym = tl.product != APPLY, last = !sym && tl.round + 1 == p.steps;
       const bool put_lo = !sym && tl.round + 1 < p.steps - 2;
       const bool mirror = sym && (tl.tj + 1) * BN <= tl.ti * kTileM;
+      const bool turn = last && tall;               // the result is stored by columns of X
+      const CUtensorMap* mo = tl.product == GRAM   ? &maps.out_a
+                              : tl.product == POLY ? &maps.out_p
+                              : last               ? &maps.out
+                                                   : &maps.out_x[(tl.round & 1) ^ 1];
       const int ld = sym ? p.ld_a : p.ld_x;
       const int row0 = tl.ti * kTileM + 128 * rank + q * 32, row = row0 + lane;
       const int n0 = tl.tj * BN + part * kCols;
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + part * kCols;
       // POLY adds b A, APPLY a lo
-      const __half* aux = tl.product == POLY ? p.a : !sym && tl.round < p.steps - 2 ? p.lo : nullptr;
-      const float aux_f = tl.product == POLY ? kB : kA;
-      const float mul = tl.product == POLY ? kC * kInvScale : last ? kInvScale * kInvScale : kInvScale;
+      const bool with_a = tl.product == POLY, with_lo = !sym && tl.round < p.steps - 2, aux = with_a || with_lo;
+      const float mul = with_a ? kC * kInvScale : last ? kInvScale * kInvScale : kInvScale;
       uint4 ah[4];
-      // a chunk's aux, coalesced: lane l loads 16-byte piece l & 3 of rows (l >> 2) + 8 i
+      // a chunk's aux, coalesced: lane l loads 16-byte piece l & 3 of rows (l >> 2) + 8 i of A,
+      // l & 1 of rows (l >> 1) + 16 i of lo
       auto fetch_aux = [&](int n) {
         if (n >= ld) return;
+        if (with_a) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = row0 + (lane >> 2) + 8 * i;
-          const size_t at = ((size_t)z * p.n + rr) * ld + n + 8 * (lane & 3);
-          ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(aux + at)) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) {
+            const int rr = row0 + (lane >> 2) + 8 * i;
+            const size_t at = ((size_t)z * p.n + rr) * ld + n + 8 * (lane & 3);
+            ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(p.a + at)) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = row0 + (lane >> 1) + 16 * i;
+            const size_t at = ((size_t)z * p.n + rr) * ld + n + 16 * (lane & 1);
+            ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(p.lo + at)) : make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       };
       if (aux) {                   // under the tile's main loop
@@ -379,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the stores from these boxes two chunks ago have read them
         if (lane == 0) gemm::bulk_wait_read<1>();
         __syncwarp();
-        if (aux) {                 // turned into one row a lane through the box
+        if (with_a) {              // turned into one row a lane through the box
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(box + box_at((lane >> 2) + 8 * i, lane & 3)) = ah[i];
@@ -391,8 +409,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-              v[4 * j + h] = f2_fma(make_float2(aux_f, aux_f), g, v[4 * j + h]);
+              v[4 * j + h] = f2_fma(make_float2(kB, kB), g, v[4 * j + h]);
             }
+          }
+          __syncwarp();
+          if (c + 32 < kCols) fetch_aux(n + 32);
+        } else if (with_lo) {
+          constexpr float f = kA / kLoScale;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(box + lo_box_at((lane >> 1) + 16 * i, lane & 1)) = ah[i];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4*>(box + lo_box_at(lane, j));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+              v[8 * j + h] = f2_fma(make_float2(f, f), unpack_e4m3x2((uint16_t)(w[h >> 1] >> 16 * (h & 1))), v[8 * j + h]);
           }
           __syncwarp();
           if (c + 32 < kCols) fetch_aux(n + 32);
@@ -405,61 +439,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (2 * i + 1 == lane && row < p.n) v[i].y += kA * kScale;
           }
         }
+        uint32_t w[16];
         if (last) {
-          bf16* res = p.result + (size_t)z * p.result_stride;
-          if (tall && !p.tma_out) {                // a warp's lanes lie along the stored rows
-            if (row < p.n)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if (n + 2 * i < p.m) res[(size_t)(n + 2 * i) * p.cols + row] = __float2bfloat16_rn(v[i].x);
-                if (n + 2 * i + 1 < p.m) res[(size_t)(n + 2 * i + 1) * p.cols + row] = __float2bfloat16_rn(v[i].y);
-              }
-            if (lane == 0) gemm::bulk_commit();
-            continue;
-          }
-          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[i].x, v[i].y);
-          if (tall) stage_turned(box, lane, w);
-          else gemm::stage_row(box, lane, w);
-          if (p.tma_out) {
-            gemm::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (row0 < p.n && n < p.m) store_3d(&maps.out, smem_u32(box), tall ? row0 : n, tall ? n : row0, z);
-              gemm::bulk_commit();
-              if (pending) signal(true);
-            }
-          } else {                 // rows at any alignment: a warp stores one row's columns at a time
-            __syncwarp();
-            for (int r = 0; r < 32 && row0 + r < p.n; ++r)
-              if (n + lane < p.m)
-                res[(size_t)(row0 + r) * p.cols + n + lane] =
-                    *reinterpret_cast<const bf16*>(box + box_at(r, lane >> 3) + (lane & 7) * 2);
-            if (lane == 0) gemm::bulk_commit();
-          }
-          continue;
-        }
-        uint32_t w[16];
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[i].x, v[i].y);
-        gemm::stage_row(box, lane, w);
-        if (mirror) stage_turned(box2, lane, w);
+          for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[i].x, v[i].y);
+        }
+        // (each form once: a launch pays for the instructions it brings in, 0.4 us of 117 here)
+        if (!turn) gemm::stage_row(box, lane, w);
+        if (mirror || turn) stage_turned(turn ? box : box2, lane, w);
         if (put_lo) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            w[i] = pack_half2(v[i].x - h.x, v[i].y - h.y);
+          for (int j = 0; j < 2; ++j) {
+            uint32_t l[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int i = 8 * j + 2 * q;
+              l[q] = pack_e4m3x4(lo_of(v[i], w[i]), lo_of(v[i + 1], w[i + 1]));
+            }
+            *reinterpret_cast<uint4*>(box2 + lo_box_at(lane, j)) = make_uint4(l[0], l[1], l[2], l[3]);
           }
-          gemm::stage_row(box2, lane, w);
+        }
+        if (last && !p.tma_out) {  // rows at any alignment: a warp stores one row's columns at a time
+          bf16* res = p.result + (size_t)z * p.result_stride;
+          __syncwarp();
+          const int r0 = turn ? n : row0, c0 = turn ? row0 : n;
+#pragma unroll 4
+          for (int r = 0; r < 32 && r0 + r < p.rows; ++r)
+            if (c0 + lane < p.cols)
+              res[(size_t)(r0 + r) * p.cols + c0 + lane] =
+                  *reinterpret_cast<const bf16*>(box + box_at(r, lane >> 3) + (lane & 7) * 2);
+          if (lane == 0) gemm::bulk_commit();
+          continue;
         }
         gemm::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const CUtensorMap* mo =
-              tl.product == GRAM ? &maps.out_a : tl.product == POLY ? &maps.out_p : &maps.out_x[(tl.round & 1) ^ 1];
-          if (row0 < p.n) {
-            store_3d(mo, smem_u32(box), n, row0, z);
+          if (row0 < p.n && (!last || n < p.m)) {
+            store_3d(mo, smem_u32(box), turn ? row0 : n, turn ? n : row0, z);
             if (put_lo) store_3d(&maps.out_lo, smem_u32(box2), n, row0, z);
           }
           // the mirror image; its rows n .. ld - 1 are the padding columns, and 0
@@ -499,18 +518,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// [batch][rows][cols] (row stride ld, matrices `apart`) of 16-bit elements; boxes of
-// box_x columns x box_y rows of one matrix, 128-byte swizzle at 64 columns, else 64-byte
+// [batch][rows][cols] (row stride ld, matrices `apart`) of 16-bit elements or bytes; boxes
+// of box_x columns x box_y rows of one matrix, swizzled over the bytes of their rows
 inline bool map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long cols, long ld, long rows, long apart,
                    int batch, int box_x, int box_y) {
+  const int size = dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2, row = box_x * size;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)apart * 2};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)apart * size};
   cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                         : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -547,7 +570,7 @@ template <int BN>
 int rounds_bn(const Work& w, char* base, bf16* out, long out_stride, int batch, int rows, int cols, int steps, int* err,
               cudaStream_t s) {
   __half* xh[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
-  __half* lo = reinterpret_cast<__half*>(base + w.lo);
+  uint8_t* lo = reinterpret_cast<uint8_t*>(base + w.lo);
   __half* a = reinterpret_cast<__half*>(base + w.a);
   __half* q = reinterpret_cast<__half*>(base + w.q);
   Maps m;
@@ -562,7 +585,8 @@ int rounds_bn(const Work& w, char* base, bf16* out, long out_stride, int batch, 
     ok = ok && x_map(&m.a_x[i], xh[i], 64, 128) && x_map(&m.b_x[i], xh[i], 64, BN / 2) &&
          x_map(&m.c_x[i], xh[i], 64, 64) && x_map(&m.out_x[i], xh[i], 32, 32);
   ok = ok && a_map(&m.a_a, a, 64, 128) && a_map(&m.b_a, a, 64, BN / 2) && a_map(&m.a_p, q, 64, 128) &&
-       x_map(&m.out_lo, lo, 32, 32) && a_map(&m.out_a, a, 32, 32) && a_map(&m.out_p, q, 32, 32);
+       map_3d(&m.out_lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, lo, w.ld_x, w.ld_x, w.n, (long)w.n * w.ld_x, batch, 32, 32) &&
+       a_map(&m.out_a, a, 32, 32) && a_map(&m.out_p, q, 32, 32);
   if (!ok) return GPT2_ERR_CUDA;
   const long apart = batch > 1 ? out_stride : (long)rows * cols;
   Params p{};

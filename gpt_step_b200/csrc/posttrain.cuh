@@ -59,14 +59,35 @@ GPT2_DEV float2 bf2_to_f2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// 2^(y - c) of a chunk's values, paired fp32 arithmetic.
+// 2^y on the fp32 pipe, relative error below 1.7e-7: y = n + f with n its nearest integer
+// (the low bits of y + 1.5 x 2^23), 2^f a polynomial of degree 5 on [-1/2, 1/2] with value 1
+// at 0 (weighted least squares of the relative error), n added to its exponent bits. y is
+// held in [-127, 127]; at -127, and so at -inf, the bits are those of 0. A NaN comes out
+// above 10^38, as an overflow does.
+GPT2_DEV float2 exp2_poly(float2 y) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n\tmin.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.x));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n\tmin.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.y));
+  auto both = [](float v) { return make_float2(v, v); };
+  const float2 t = f2_add(y, both(12582912.f)), n = f2_add(t, both(-12582912.f)), f = f2_fma(n, both(-1.f), y);
+  float2 p = f2_fma(both(1.326472731e-03f), f, both(9.671512991e-03f));
+  p = f2_fma(p, f, both(5.550733581e-02f));
+  p = f2_fma(p, f, both(2.402224243e-01f));
+  p = f2_fma(p, f, both(6.931470037e-01f));
+  p = f2_fma(p, f, both(1.f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// 2^(y - c) of a chunk's values, paired fp32 arithmetic; MIX: a quarter of them on the fp32
+// pipe (overflows and NaN as there).
+template <bool MIX = false>
 GPT2_DEV void chunk_exp(uint4 u, float c, float2 (&e)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   const float2 l2 = make_float2(k::kLog2eF, k::kLog2eF), nc = make_float2(-c, -c);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 y = f2_fma(bf2_to_f2(w[j]), l2, nc);
-    e[j] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    e[j] = MIX && j == 3 ? exp2_poly(y) : make_float2(ex2_approx(y.x), ex2_approx(y.y));
   }
 }
 
@@ -315,12 +336,14 @@ struct RowPipe {
     flip ^= 1;
     return warp_sum(v);
   }
-  // sum of 2^(y - c); with `zn` the slots take the next row on the way.
+  // sum of 2^(y - c); with `zn` the slots take the next row on the way. MIX: a sum from
+  // kSumMax on stands for an overflow or a NaN too.
+  template <bool MIX>
   GPT2_DEV float sum_from(float c, const uint4* zn) {
     float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
     auto add = [&](uint4 u) {
       float2 e[4];
-      chunk_exp(u, c, e);
+      chunk_exp<MIX>(u, c, e);
       acc0 = f2_add(acc0, f2_add(e[0], e[1]));
       acc1 = f2_add(acc1, f2_add(e[2], e[3]));
     };
@@ -405,7 +428,7 @@ __global__ void __launch_bounds__(32 * G, 32 / G) policy_loss_kernel(const Polic
     const int t = cur.t;
     const float zt = cur.zt;
     pipe.arrive(a.V);
-    float c = zt * k::kLog2eF, s = pipe.sum_from(c, nullptr);
+    float c = zt * k::kLog2eF, s = pipe.template sum_from<true>(c, nullptr);
     if (!(s < kSumMax)) {   // (the same in every thread)
       __nv_bfloat162 m2 = as_bf2(kNegInf2);
       for (int i = threadIdx.x; i < pipe.nvr; i += 32 * G) m2 = __hmax2(m2, chunk_max(row_slots[i]));
@@ -417,7 +440,7 @@ __global__ void __launch_bounds__(32 * G, 32 / G) policy_loss_kernel(const Polic
         m = warp_max(lane < G ? red_m[lane] : -INFINITY);
       }
       c = m * k::kLog2eF;
-      s = pipe.sum_from(c, nullptr);
+      s = pipe.template sum_from<false>(c, nullptr);
     }
     const float lp = row_logp(zt, c, s);
     float loss, g;
@@ -502,6 +525,11 @@ struct RowArgs {
 };
 
 // Rows' lp (0 for rows left out) and (c, S); rows outside the sequences are passed over.
+// The ex2 pipe is 60% busy here, in bursts between a row's arrivals: a quarter of the
+// exponentials on the fp32 pipe takes the preference loss of 9 pairs of 1,024 x 50,257 from
+// 747 us to 735, half of them to 765. The policy loss sums the same way, for the same bits
+// (19,456 x 50,257: 622 us against 626, 16,384 x 4,353: 54.2 against 53.7); a quarter of its
+// gradient's exponentials too would cost it 30 us.
 template <int G>
 __global__ void __launch_bounds__(32 * G, 32 / G) row_logp_kernel(const RowArgs a) {
   extern __shared__ __align__(128) uint4 row_slots[];
@@ -537,7 +565,7 @@ __global__ void __launch_bounds__(32 * G, 32 / G) row_logp_kernel(const RowArgs 
     const float zt_next = __shfl_sync(0xffffffffu, win.zt, max(j, 0));
     const uint4* zn = j >= 0 ? reinterpret_cast<const uint4*>(a.logits + (size_t)next * a.Vp) : nullptr;
     pipe.arrive(a.V);
-    float c = zt * k::kLog2eF, s = pipe.sum_from(c, zn);
+    float c = zt * k::kLog2eF, s = pipe.template sum_from<true>(c, zn);
     if (!(s < kSumMax))   // (the same in every thread) the slots have moved on
       streamed_stats<G>(reinterpret_cast<const uint4*>(a.logits + (size_t)row * a.Vp), a.V, c, s);
     if (threadIdx.x == 0) {

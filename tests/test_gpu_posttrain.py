@@ -289,6 +289,34 @@ def test_token_logps():
         assert np.all(np.abs(host(out) - lp) <= lp_tol(lp)) and int(err.sum()) == 0
 
 
+@pytest.mark.parametrize("V,Vp", [(30, 32), (1000, 1024), (9001, 9008), (50257, 50304)])
+def test_token_logps_of_rows_with_infinities_and_nan(V, Vp):
+    """At every place of a 16-byte piece: -inf has probability 0, a NaN or +inf gives no number."""
+    rng = np.random.default_rng(V)
+    N = 40
+    z = rng.standard_normal((N, Vp)) * 1.5
+    z[:, V:] = np.nan                                # padded ids are not read
+    t = rng.integers(0, 8, N)
+    at = V - 9 - np.arange(8)
+    for i in range(8):
+        z[i, at[i]] = -np.inf
+        z[8 + i, at[i]] = np.nan
+        z[16 + i, at[i]] = np.inf
+    z[24:32, 8:V] = -np.inf                          # eight ids left
+    z[32:36, t[32]] = z[32:36, :V].max() + 130.0     # the others below 2^-127 of the target
+    t[32:36] = t[32]
+    t[36:] = at[0]
+    z[36:, 3] = 250.0                                # the target's log-probability is below -230
+    zd = bf16(z)
+    out, err = torch.empty(N, device="cuda"), err_word()
+    gs.token_logps(zd, i32(t), out, V, err)
+    got = host(out)
+    assert np.isnan(got[8:24]).all()
+    fine = np.r_[0:8, 24:N]
+    lp, _, _ = PT.token_logps(host(zd)[fine], t[fine], V)
+    assert np.all(np.abs(got[fine] - lp) <= lp_tol(lp))
+
+
 # -- Newton-Schulz -----------------------------------------------------------------------------
 
 # Bound of the result (relative, Frobenius): bf16 rounding, at most half a step 2^-8 = 3.9e-3; X's

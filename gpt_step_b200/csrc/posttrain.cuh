@@ -618,8 +618,8 @@ struct PairArgs {
 
 // The preference loss reads the logits twice, in row_logp_kernel and pair_grad_kernel: no
 // row's gradient is known before all rows of its pair are. A pair of the largest case (two
-// sequences of 1,024 x 50,257) is more than L2 holds. Nine such pairs: 717 to 754 us by box, 4.4 TB/s of
-// the bytes needed once and 6.2 TB/s of those moved; eight pairs of up to 2 x 1,024 x 4,353:
+// sequences of 1,024 x 50,257) is more than L2 holds. Nine such pairs: 723 us, 4.4 TB/s of
+// the bytes needed once and 6.1 TB/s of those moved; eight pairs of up to 2 x 1,024 x 4,353:
 // 56 us. One cooperative launch with grid barriers between the steps, and groups of pairs
 // that L2 holds, measured 921 and 100 us.
 
@@ -732,7 +732,9 @@ GPT2_DEV int find_sequence(const int32_t* start, int n_seq, int row) {
 // The rows' gradients from their (c, S): a warp a row where G is 1 (four a CTA), else the
 // CTA's G warps. OWN: the first n_seq / 2 CTAs take the pairs, and every other CTA adds up
 // its rows' pair for itself, a few thousand log-probabilities out of L2, instead of waiting
-// for a launch between (pa.coef otherwise holds the coefficients).
+// for a launch between (pa.coef otherwise holds the coefficients). Rows in descending order:
+// the last ones of row_logp_kernel's pass are still in L2 (9 pairs of 1,024 x 50,257: 723 us
+// against 733).
 template <int G, bool OWN>
 __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const PairGradArgs a, const PairArgs pa) {
   constexpr int kRows = G == 1 ? 4 : 1, T = G == 1 ? 128 : 32 * G;
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const 
     return;
   }
   const int w = G == 1 ? threadIdx.x >> 5 : 0, lane = G == 1 ? lane_id() : threadIdx.x;
-  const long row = (long)(blockIdx.x - P) * kRows + w;
+  const long row = (long)(gridDim.x - 1 - blockIdx.x) * kRows + w;
   int seq = -1, t = 0;
   bool kept = false;
   if (row < a.N) {

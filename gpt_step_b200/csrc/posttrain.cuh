@@ -369,8 +369,8 @@ struct RowPipe {
 
 // The policy loss: a row is read from memory once and its gradient written once, which is
 // what bounds it. 19,456 x 50,257 with a quarter of the rows left out: 598 to 627 us by box, 5.7 TB/s of
-// the bytes it cannot do without (0.87 of the measured copy rate); the ex2 pipe is 55% busy
-// beside it, at two exponentials an element. Measured before: the row read twice, the second
+// the bytes it cannot do without (0.87 of the measured copy rate); the ex2 pipe is 49% busy
+// beside it, at 1.75 of them an element. Measured before: the row read twice, the second
 // time out of L2, 727 us (eight CTAs an SM bring more rows than L2 holds); held in registers
 // by 512 threads 678 us; in shared memory by one bulk copy a row, with a pass for the
 // maximum, 657 us. 16,384 x 4,353: 54 us, 0.72; there a row is short and its fixed part
@@ -525,8 +525,8 @@ struct RowArgs {
 };
 
 // Rows' lp (0 for rows left out) and (c, S); rows outside the sequences are passed over.
-// The ex2 pipe is 60% busy here, in bursts between a row's arrivals: a quarter of the
-// exponentials on the fp32 pipe takes the preference loss of 9 pairs of 1,024 x 50,257 from
+// With all exponentials on it the ex2 pipe is 60% busy here, in bursts between a row's
+// arrivals: a quarter of them on the fp32 pipe takes the preference loss of 9 pairs of 1,024 x 50,257 from
 // 747 us to 735, half of them to 765. The policy loss sums the same way, for the same bits
 // (19,456 x 50,257: 622 us against 626, 16,384 x 4,353: 54.2 against 53.7); a quarter of its
 // gradient's exponentials too would cost it 30 us.

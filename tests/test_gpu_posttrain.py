@@ -243,6 +243,13 @@ def test_preference_loss(P, most, V, Vp, kind, average, smoothing, inplace):
     assert np.array_equal(got[~inside], untouched, equal_nan=True)
 
 
+# pairs of few rows of medium length; long pairs, whose coefficients take a launch of their own
+@pytest.mark.parametrize("P,most,V,Vp", [(3, 60, 5001, 5008), (2, 1500, 4700, 4704), (2, 4000, 37, 40)])
+@pytest.mark.parametrize("kind,average,smoothing,inplace", [("sigmoid", True, 0.2, True), ("squared", False, 0.0, False)])
+def test_preference_loss_by_pair_length(P, most, V, Vp, kind, average, smoothing, inplace):
+    test_preference_loss(P, most, V, Vp, kind, average, smoothing, inplace)
+
+
 def test_preference_loss_of_many_rows_and_without_a_gradient():
     """More rows than the gradient's launch takes on the pairs as well, and losses alone."""
     N, V, Vp, P = 33000, 40, 40, 3

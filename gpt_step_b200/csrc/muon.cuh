@@ -11,11 +11,16 @@
 // rounding error that lies along them. With bf16 operands the result is 1% (a
 // flat spectrum) to 4% (a falling one) off; fp16 operands have three more bits
 // at the same tensor rate and their range is enough, because every element of X,
-// A, P is bounded (1.21, 1.46, 16): they are held times 2^10. X is held as two
-// numbers (hi + lo, fp16 and what it leaves) in all but the last two rounds: the tensor
-// cores see hi alone, and a lo, its part in the term a X along which the growth happens, is added
-// in fp32. That ends 0.1% off for either spectrum (0.5% without lo) for no more
-// matrix instructions, below the 0.17% of the bf16 result's own rounding.
+// A, P is bounded (1.21, 1.46, 16): they are held times 2^10. X is held as two fp16
+// numbers (hi + lo, 22 bits) in all but the last two rounds: the tensor cores see hi
+// alone, and a lo, its part in the term a X along which the growth happens, is added
+// in fp32, for no more matrix instructions. Five rounds then end 0.10 to 0.13% off on spectra
+// that are flat or fall like 1/k (0.5% without lo) and 0.15 to 0.21% on steeper ones (1/k^2,
+// e^(-k/20); 2% and 1.5% without), beside the 0.17% of the bf16 result's own rounding. lo
+// needs its fp16: with e4m3, half the bytes and 3% less time for large matrices, eight rounds on
+// the steep spectra ended 0.6 to 0.9% off, the result's rounding included, instead of 0.22 to 0.38%.
+// From eight rounds on the fp32 sums of P X count too: what they leave grows by up to 3.44 a
+// round (1,536 rows, e^(-k/20): 0.27% after five rounds, 0.38% after eight, 2.4% after ten).
 #pragma once
 #include <cuda_fp16.h>
 
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(256) ns_sumsq_kernel(const T* __restrict__ x, 
 }
 
 // ---------------------------------------------------------------------------
-// X = M / (|M|_F + 1e-7), times 2^10, as hi (fp16) and lo (e4m3) [batch][n][ld], padding 0;
+// X = M / (|M|_F + 1e-7), times 2^10, as hi and lo [batch][n][ld] fp16, padding 0;
 // and the counters of the rounds at 0. A thread forms 8 columns of a row; tall matrices
 // come through shared memory, 64 x 64 at a time.
 // ---------------------------------------------------------------------------
@@ -92,29 +97,6 @@ GPT2_DEV void split8(const float* f, uint4& hi, uint4& lo) {
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-// The lo that goes through memory: e4m3 of 2^8 lo. hi is good to 11 bits and |lo| <= 0.5, so
-// the largest is 128 of e4m3's 448, and hi + lo still has 15 bits; the result's error stays
-// the same to two digits (1.8e-3 on a spectrum falling like e^(-i/20), 1.1e-2 without lo), and
-// lo is half the bytes of fp16 (12 x 2,304 x 768: 461 us to 446, 16 x 1,536 x 6,144: 4.44 ms to
-// 4.32). A matrix that stays on chip keeps it in fp16.
-constexpr float kLoScale = 256.f;
-GPT2_DEV uint32_t pack_e4m3x4(float2 a, float2 b) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
-  return (uint32_t)lo | (uint32_t)hi << 16;
-}
-GPT2_DEV float2 unpack_e4m3x2(uint16_t u) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-// 2^8 (a - hi), hi a's fp16 values
-GPT2_DEV float2 lo_of(float2 a, uint32_t hi) {
-  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return make_float2((a.x - h.x) * kLoScale, (a.y - h.y) * kLoScale);
 }
 
 // Eight neighbouring elements, in 16-byte loads if `vec`; those from `valid` on are 0.
@@ -138,7 +120,7 @@ GPT2_DEV void load8(const T* p, int valid, bool vec, float (&f)[8]) {
 template <typename T, bool TALL>
 __global__ void __launch_bounds__(256) ns_convert_kernel(const T* __restrict__ x, long stride, int rows, int cols,
                                                          const double* __restrict__ part, int parts,
-                                                         __half* __restrict__ hi, uint8_t* __restrict__ lo, int ld,
+                                                         __half* __restrict__ hi, __half* __restrict__ lo, int ld,
                                                          int vec, uint32_t* __restrict__ count) {
   pdl_begin();
   __shared__ float tile[TALL ? 64 : 1][65];
@@ -158,16 +140,11 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const T* __restrict__ x
   auto put = [&](int r, int c, float (&f)[8]) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[q] *= mul;
-    uint32_t h[4];
-    float2 l[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[q] = pack_half2(f[2 * q], f[2 * q + 1]);
-      l[q] = lo_of(make_float2(f[2 * q], f[2 * q + 1]), h[q]);
-    }
+    uint4 h, l;
+    split8(f, h, l);
     const size_t at = ((size_t)z * n + r) * ld + c;
-    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint2*>(lo + at) = make_uint2(pack_e4m3x4(l[0], l[1]), pack_e4m3x4(l[2], l[3]));
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
   };
   if (!TALL) {
     const int per_row = ld / 8;
@@ -239,7 +216,7 @@ inline bool plan(int batch, int rows, int cols, Work* w) {
   const size_t xb = (size_t)batch * w->n * w->ld_x * 2, ab = (size_t)batch * w->n * w->ld_a * 2;
   w->x0 = take(xb);
   w->x1 = take(xb);
-  w->lo = take(xb / 2);
+  w->lo = take(xb);
   w->a = take(ab);
   w->q = take(ab);
   w->part = take((size_t)batch * w->parts * 8);
@@ -260,7 +237,7 @@ cudaError_t prepare_x(const Work& w, char* base, const T* x, long x_stride, int 
     if (e != cudaSuccess) return e;
   }
   __half* hi = reinterpret_cast<__half*>(base + w.x0);
-  uint8_t* lo = reinterpret_cast<uint8_t*>(base + w.lo);
+  __half* lo = reinterpret_cast<__half*>(base + w.lo);
   uint32_t* count = reinterpret_cast<uint32_t*>(base + w.count);
   const bool tall = rows > cols;
   const int vec_rows = vec && (cols * sizeof(T)) % 16 == 0;   // every row of M begins on 16 bytes

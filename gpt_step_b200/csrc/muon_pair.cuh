@@ -18,16 +18,16 @@
 // reads nothing but lo.
 //
 // What bounds it: large matrices the tensor pipe under the power limit (16 x 1,536 x 6,144:
-// 4.06 to 4.32 ms by box, 0.87 to 0.93 PFLOP/s of the products with symmetric ones counted half); 768 rows the
+// 4.36 to 4.40 ms, 0.86 PFLOP/s of the products with symmetric ones counted half); 768 rows the
 // shared memory, whose bandwidth the operands take whole at the full tensor rate (64 bytes a
-// clock in and out) and an APPLY tile's hi, lo and aux boxes a third as much again (tile 6.4 us
-// against 4.5 of main loop when lo was fp16; 12 x 2,304 x 768: 446 us); small ones the
+// clock in and out) and an APPLY tile's hi, lo and aux boxes half as much again (tile 6.4 us
+// against 4.5 of main loop; 12 x 2,304 x 768: 458 us); small ones the
 // latency of a product, 5 to 7 us: loads and MMA 1.8, epilogue 2, its stores in memory and
-// seen by the next product 1.5 (3 x 333 x 517: 116 us; 124 with a second proxy fence before a
-// finished tile's signal, when the following were measured). Measured and rejected: results
+// seen by the next product 1.5 (3 x 333 x 517: 117 us). Measured and rejected, against 124 us
+// and 461 us of the kernel as it was then: results
 // by 16-byte stores out of the boxes (3 x 333 x 517 145 us, 12 x 2,304 x 768 500 us), by
 // 32-byte stores of a row a lane (144, 575), sixteen epilogue warps with a box each (139,
-// 483); three launches a round (146 us and, with the same preparation, about 440).
+// 483), three launches a round (146, 483).
 #pragma once
 #include "gemm2sm.cuh"
 #include "muon.cuh"
@@ -52,14 +52,13 @@ enum Product : int { GRAM = 0, POLY = 1, APPLY = 2 };
 struct Maps {
   CUtensorMap a_x[2], b_x[2], c_x[2];   // X by rows of 128, by rows of BN / 2, by 64 x 64 columns
   CUtensorMap a_a, b_a, a_p;            // A by rows (both operands), P by rows
-  CUtensorMap out_x[2], out_lo, out_a, out_p, out;   // boxes of 32 x 32 (lo: bytes)
+  CUtensorMap out_x[2], out_lo, out_a, out_p, out;   // boxes of 32 x 32
 };
 
 struct Params {
   int n, m, ld_x, ld_a, batch, steps;
   int tiles_m, sym, full;               // row tiles; tiles of a symmetric product, of the last one
-  const uint8_t* lo;                    // [batch][n][ld_x] e4m3
-  const __half* a;
+  const __half *lo, *a;
   uint32_t* count;                      // [batch][3] signals of finished tiles
   bf16* result;
   long result_stride;
@@ -166,9 +165,6 @@ GPT2_DEV bool wait_ready(uint32_t at, uint32_t k, int* err) {
 
 // 16-byte chunk j of row r in a 32 x 32 box of 64-byte rows, 64-byte swizzle.
 GPT2_DEV uint32_t box_at(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
-
-// The same of a box of 32-byte rows, 32-byte swizzle.
-GPT2_DEV uint32_t lo_box_at(int r, int j) { return (uint32_t)(r * 32 + ((j ^ ((r >> 2) & 1)) << 4)); }
 
 // A lane's 32 values (its row) down a column of the box: the box turned over.
 GPT2_DEV void stage_turned(uint8_t* box, int lane, const uint32_t (&w)[16]) {
@@ -347,27 +343,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n0 = tl.tj * BN + part * kCols;
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + part * kCols;
       // POLY adds b A, APPLY a lo
-      const bool with_a = tl.product == POLY, with_lo = !sym && tl.round < p.steps - 2, aux = with_a || with_lo;
-      const float mul = with_a ? kC * kInvScale : last ? kInvScale * kInvScale : kInvScale;
+      const __half* aux = tl.product == POLY ? p.a : !sym && tl.round < p.steps - 2 ? p.lo : nullptr;
+      const float aux_f = tl.product == POLY ? kB : kA;
+      const float mul = tl.product == POLY ? kC * kInvScale : last ? kInvScale * kInvScale : kInvScale;
       uint4 ah[4];
-      // a chunk's aux, coalesced: lane l loads 16-byte piece l & 3 of rows (l >> 2) + 8 i of A,
-      // l & 1 of rows (l >> 1) + 16 i of lo
+      // a chunk's aux, coalesced: lane l loads 16-byte piece l & 3 of rows (l >> 2) + 8 i
       auto fetch_aux = [&](int n) {
         if (n >= ld) return;
-        if (with_a) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = row0 + (lane >> 2) + 8 * i;
-            const size_t at = ((size_t)z * p.n + rr) * ld + n + 8 * (lane & 3);
-            ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(p.a + at)) : make_uint4(0u, 0u, 0u, 0u);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rr = row0 + (lane >> 1) + 16 * i;
-            const size_t at = ((size_t)z * p.n + rr) * ld + n + 16 * (lane & 1);
-            ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(p.lo + at)) : make_uint4(0u, 0u, 0u, 0u);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int rr = row0 + (lane >> 2) + 8 * i;
+          const size_t at = ((size_t)z * p.n + rr) * ld + n + 8 * (lane & 3);
+          ah[i] = rr < p.n ? __ldcg(reinterpret_cast<const uint4*>(aux + at)) : make_uint4(0u, 0u, 0u, 0u);
         }
       };
       if (aux) {                   // under the tile's main loop
@@ -397,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the stores from these boxes two chunks ago have read them
         if (lane == 0) gemm::bulk_wait_read<1>();
         __syncwarp();
-        if (with_a) {              // turned into one row a lane through the box
+        if (aux) {                 // turned into one row a lane through the box
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(box + box_at((lane >> 2) + 8 * i, lane & 3)) = ah[i];
@@ -409,24 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-              v[4 * j + h] = f2_fma(make_float2(kB, kB), g, v[4 * j + h]);
+              v[4 * j + h] = f2_fma(make_float2(aux_f, aux_f), g, v[4 * j + h]);
             }
-          }
-          __syncwarp();
-          if (c + 32 < kCols) fetch_aux(n + 32);
-        } else if (with_lo) {
-          constexpr float f = kA / kLoScale;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<uint4*>(box + lo_box_at((lane >> 1) + 16 * i, lane & 1)) = ah[i];
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 u = *reinterpret_cast<const uint4*>(box + lo_box_at(lane, j));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int h = 0; h < 8; ++h)
-              v[8 * j + h] = f2_fma(make_float2(f, f), unpack_e4m3x2((uint16_t)(w[h >> 1] >> 16 * (h & 1))), v[8 * j + h]);
           }
           __syncwarp();
           if (c + 32 < kCols) fetch_aux(n + 32);
@@ -452,15 +423,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (mirror || turn) stage_turned(turn ? box : box2, lane, w);
         if (put_lo) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t l[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int i = 8 * j + 2 * q;
-              l[q] = pack_e4m3x4(lo_of(v[i], w[i]), lo_of(v[i + 1], w[i + 1]));
-            }
-            *reinterpret_cast<uint4*>(box2 + lo_box_at(lane, j)) = make_uint4(l[0], l[1], l[2], l[3]);
+          for (int i = 0; i < 16; ++i) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            w[i] = pack_half2(v[i].x - h.x, v[i].y - h.y);
           }
+          gemm::stage_row(box2, lane, w);
         }
         if (last && !p.tma_out) {  // rows at any alignment: a warp stores one row's columns at a time
           bf16* res = p.result + (size_t)z * p.result_stride;
@@ -518,22 +485,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// [batch][rows][cols] (row stride ld, matrices `apart`) of 16-bit elements or bytes; boxes
-// of box_x columns x box_y rows of one matrix, swizzled over the bytes of their rows
+// [batch][rows][cols] (row stride ld, matrices `apart`) of 16-bit elements; boxes of
+// box_x columns x box_y rows of one matrix, 128-byte swizzle at 64 columns, else 64-byte
 inline bool map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long cols, long ld, long rows, long apart,
                    int batch, int box_x, int box_y) {
-  const int size = dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2, row = box_x * size;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)apart * size};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)apart * 2};
   cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-             : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                         : CU_TENSOR_MAP_SWIZZLE_32B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -570,7 +533,7 @@ template <int BN>
 int rounds_bn(const Work& w, char* base, bf16* out, long out_stride, int batch, int rows, int cols, int steps, int* err,
               cudaStream_t s) {
   __half* xh[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
-  uint8_t* lo = reinterpret_cast<uint8_t*>(base + w.lo);
+  __half* lo = reinterpret_cast<__half*>(base + w.lo);
   __half* a = reinterpret_cast<__half*>(base + w.a);
   __half* q = reinterpret_cast<__half*>(base + w.q);
   Maps m;
@@ -585,8 +548,7 @@ int rounds_bn(const Work& w, char* base, bf16* out, long out_stride, int batch, 
     ok = ok && x_map(&m.a_x[i], xh[i], 64, 128) && x_map(&m.b_x[i], xh[i], 64, BN / 2) &&
          x_map(&m.c_x[i], xh[i], 64, 64) && x_map(&m.out_x[i], xh[i], 32, 32);
   ok = ok && a_map(&m.a_a, a, 64, 128) && a_map(&m.b_a, a, 64, BN / 2) && a_map(&m.a_p, q, 64, 128) &&
-       map_3d(&m.out_lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, lo, w.ld_x, w.ld_x, w.n, (long)w.n * w.ld_x, batch, 32, 32) &&
-       a_map(&m.out_a, a, 32, 32) && a_map(&m.out_p, q, 32, 32);
+       x_map(&m.out_lo, lo, 32, 32) && a_map(&m.out_a, a, 32, 32) && a_map(&m.out_p, q, 32, 32);
   if (!ok) return GPT2_ERR_CUDA;
   const long apart = batch > 1 ? out_stride : (long)rows * cols;
   Params p{};

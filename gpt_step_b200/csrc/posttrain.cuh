@@ -227,14 +227,22 @@ struct PolicyArgs {
   int* err;
 };
 
+// r held in [lo, hi]; a NaN stays one.
+GPT2_DEV float clip_nan(float r, float lo, float hi) {
+  asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
 // The row's loss and g = dscale dloss/dlp.
 GPT2_DEV void policy_row(const PolicyArgs& a, float lp, float old_lp, float adv, float ref, float w, float& loss,
                          float& g) {
   const float r = expf(lp - old_lp);
-  // r A and its clipped form; an advantage of 0 gives 0 for any ratio
-  const float free_s = adv == 0.f ? 0.f : r * adv;
-  const float cut_s = fminf(fmaxf(r, 1.f - a.clip_low), 1.f + a.clip_high) * adv;
-  const bool active = free_s <= cut_s;
+  // r A and its clipped form; an advantage of 0 gives 0 for any ratio, but does not hide that
+  // the row has no log-probability
+  const bool none = adv == 0.f && !isnan(lp);
+  const float free_s = none ? 0.f : r * adv;
+  const float cut_s = none ? 0.f : clip_nan(r, 1.f - a.clip_low, 1.f + a.clip_high) * adv;
+  const bool active = !(free_s > cut_s);   // a NaN goes on into the loss and the gradient
   loss = active ? -free_s : -cut_s;
   g = active ? -free_s : 0.f;
   if (a.ref_logp) {

@@ -206,7 +206,8 @@ int gpt2op_token_logps(const void* logits, const int32_t* targets, float* logps,
  *   losses = weight * ( -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
  *                       + kl_coef * (e^d - d - 1) )
  *   dlosses/dlp = weight * ( -[r A <= clip(r) A] r A + kl_coef * (1 - e^d) ).
- * An advantage A of 0 gives 0 for any r. old_logp, adv, weight (NULL: 1), ref_logp
+ * An advantage A of 0 gives 0 for any r; any other NaN, of a kept row's logits or
+ * inputs, is a NaN in its loss and gradient. old_logp, adv, weight (NULL: 1), ref_logp
  * (NULL with kl_coef 0) fp32 [N]; logps (may be NULL) and losses fp32 [N].
  * 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, all finite. */
 int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* old_logp, const float* ref_logp,

@@ -36,12 +36,14 @@ def logit_gradient(p, targets, keep, g, Vp):
 
 
 def policy_rows(lp, old, adv, ref, w, clip_low, clip_high, kl):
-    """Per-row loss and its derivative by lp."""
-    r = np.exp(lp - old)
-    free = np.where(adv == 0, 0.0, r * adv)
-    cut = np.clip(r, 1 - clip_low, 1 + clip_high) * adv
+    """Per-row loss and its derivative by lp; an advantage of 0 gives 0 for any ratio, any other NaN is a NaN in both."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        r = np.exp(lp - old)
+        none = (adv == 0) & ~np.isnan(lp)
+        free = np.where(none, 0.0, r * adv)
+        cut = np.where(none, 0.0, np.clip(r, 1 - clip_low, 1 + clip_high) * adv)
     loss = -np.minimum(free, cut)
-    g = np.where(free <= cut, -free, 0.0)
+    g = np.where(free > cut, 0.0, -free)
     if ref is not None and kl:
         d = ref - lp
         loss = loss + kl * (np.expm1(d) - d)

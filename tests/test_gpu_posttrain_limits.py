@@ -1,0 +1,83 @@
+"""The post-training losses where numbers end: NaN and infinities in logits and inputs.
+
+What has a finite value is held to the bounds of test_gpu_posttrain.py (`lp_tol`,
+`grad_tol`); what has none must not look as if it had.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import gpt_step_b200 as gs
+from oracle import posttrain as PT
+
+from gpu_util import bf16, err_word, f32, host, i32, require_gpu, torch
+from test_gpu_posttrain import grad_tol, lp_tol, rows_case
+
+pytestmark = pytest.mark.gpu
+
+# a row by one warp, by sixteen, and from global memory
+WIDTHS = [(40, 48), (1000, 1024), (5000, 5008), (50257, 50304), (120001, 120008)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def policy(z, t, V, old, adv, grad=True, **kw):
+    N, Vp = z.shape
+    dz = torch.full((N, Vp), 7.0, dtype=torch.bfloat16, device="cuda") if grad else None
+    logps, losses, err = torch.full((N,), 7.0, device="cuda"), torch.full((N,), 7.0, device="cuda"), err_word()
+    gs.policy_loss(bf16(z), i32(t), f32(old), f32(adv), dz, logps, losses, V, err,
+                   **{k: f32(v) if isinstance(v, np.ndarray) else v for k, v in kw.items()})
+    assert int(err.sum()) == 0
+    return host(logps), host(losses), host(dz) if grad else None
+
+
+@pytest.mark.parametrize("V,Vp", WIDTHS)
+def test_policy_loss_of_numbers_that_are_none(V, Vp):
+    """A NaN anywhere in a kept row's formula is a NaN in its loss and its gradient."""
+    rng, z, t = rows_case(9, V, Vp, V, masked=0.0)
+    lp, _, _ = PT.token_logps(z, t, V)
+    adv = np.array([1.0, -1.0, 1.0, 1.0, 0.0, 0.0, 1.0, -2.0, 1.0])
+    old = lp.astype(np.float32).astype(np.float64)
+    ref, w = old.copy(), np.ones(9)
+    z[0, (t[0] + 1) % V] = np.nan              # the row's logits
+    z[1, t[1]] = np.nan
+    old[2] = np.nan                            # the sampling policy's log-probability
+    adv[3] = np.nan
+    z[4, (t[4] + 1) % V] = np.nan              # an advantage of 0 does not hide the row's own logits
+    old[5] = np.nan                            # but it gives 0 for any ratio
+    w[6] = np.nan
+    bad = [0, 1, 2, 3, 4, 6]
+    got_lp, loss, dz = policy(z, t, V, old, adv, weight=w)
+    assert np.isnan(loss[bad]).all() and np.isnan(dz[bad][:, :V]).all() and np.all(dz[:, V:] == 0)
+    assert np.isnan(got_lp[[0, 1, 4]]).all()
+    fine = [2, 3, 5, 6, 7, 8]
+    assert np.all(np.abs(got_lp - lp)[fine] <= lp_tol(lp)[fine])
+    assert loss[5] == 0 and np.all(dz[5] == 0)
+    rl, _, rdz = PT.policy_loss(z[7:], t[7:], V, old[7:], adv[7:])
+    # the ratio is 1 within the log-probability's bound
+    assert np.all(np.abs(loss[7:] - rl) <= 2 * np.abs(adv[7:]) * (lp_tol(lp[7:]) + 2.0 ** -23))
+    assert np.all(np.abs(dz[7:] - rdz) <= grad_tol(rdz, np.abs(adv[7:])))
+    # the losses alone, and with a KL term whose reference is a NaN too
+    assert np.isnan(policy(z, t, V, old, adv, grad=False, weight=w)[1][bad]).all()
+    ref[8] = np.nan
+    _, loss, dz = policy(z, t, V, old, adv, weight=w, ref_logp=ref, kl_coef=0.1)
+    bad.append(8)
+    assert np.isnan(loss[bad]).all() and np.isnan(dz[bad][:, :V]).all() and np.isfinite(loss[[5, 7]]).all()
+
+
+@pytest.mark.parametrize("V,Vp", WIDTHS)
+def test_oracle_and_kernel_agree_on_infinite_ratios(V, Vp):
+    """old_logp of -inf and +inf, an advantage of 0 among them: losses as defined, none a NaN."""
+    _, z, t = rows_case(6, V, Vp, V + 1, masked=0.0)
+    old = np.array([-np.inf, -np.inf, np.inf, np.inf, -np.inf, np.inf])
+    adv = np.array([1.0, -1.0, 1.0, -1.0, 0.0, 0.0])
+    with np.errstate(invalid="ignore"):
+        rl, _, rdz = PT.policy_loss(z, t, V, old, adv)
+    _, loss, dz = policy(z, t, V, old, adv)
+    rest = np.isfinite(rl)
+    assert np.all(loss[~rest] == rl[~rest]) and np.all(np.abs(loss - rl)[rest] <= 2.0 ** -23 * np.abs(rl)[rest])
+    assert np.all(dz[rest] == rdz[rest]) and loss[1] == np.inf

@@ -1,0 +1,24 @@
+"""The post-training definitions where numbers end, on the CPU."""
+import numpy as np
+
+from oracle import posttrain as PT
+
+
+def rows(**kw):
+    a = dict(lp=-1.0, old=-1.0, adv=1.0, ref=None, w=1.0)
+    a.update(kw)
+    n = 1
+    f = lambda v: None if v is None else np.full(n, v)  # noqa: E731
+    with np.errstate(invalid="ignore"):
+        loss, g = PT.policy_rows(f(a["lp"]), f(a["old"]), f(a["adv"]), f(a["ref"]), f(a["w"]), 0.2, 0.2,
+                                 0.1 if a["ref"] is not None else 0.0)
+    return float(loss[0]), float(g[0])
+
+
+def test_a_policy_row_with_a_nan_has_no_loss_and_no_slope():
+    nan, inf = np.nan, np.inf
+    for bad in (dict(lp=nan), dict(old=nan), dict(adv=nan), dict(w=nan), dict(ref=nan), dict(lp=nan, adv=0.0),
+                dict(lp=-inf, old=-inf)):
+        assert all(np.isnan(rows(**bad))), bad
+    for fine in (dict(old=nan), dict(old=-inf), dict(old=inf), dict(lp=-inf, old=-inf)):
+        assert rows(adv=0.0, **fine) == (0.0, 0.0), fine      # an advantage of 0 gives 0 for any ratio

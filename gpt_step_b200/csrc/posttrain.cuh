@@ -18,12 +18,20 @@ namespace pt {
 constexpr int kPairThreads = 256;
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;   // two bf16 -inf
 
+// (c, S) joined with another. Where both maxima are -inf the sums hold no numbers, 0 or, of
+// values that are all NaN, a NaN that must not be lost.
+GPT2_DEV void join_stats(float& c, float& s, float oc, float os) {
+  const float m = fmaxf(c, oc);
+  s = m == -INFINITY ? s + os : s * ex2_approx(c - m) + os * ex2_approx(oc - m);
+  c = m;
+}
+
 // (c, S) of a row split over `G` warps, from each lane's own pair.
 template <int G>
 GPT2_DEV void combine_stats(float& c, float& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    k::ce_combine(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
+    join_stats(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
   if (G > 1) {
     __shared__ float2 red[G];
     if (lane_id() == 0) red[threadIdx.x >> 5] = make_float2(c, s);
@@ -33,7 +41,7 @@ GPT2_DEV void combine_stats(float& c, float& s) {
     s = v.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      k::ce_combine(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
+      join_stats(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
   }
 }
 
@@ -206,7 +214,7 @@ GPT2_DEV void part_stats(const float2* part, int slots, int lane, float& c, floa
   s = 0.f;
   for (int i = lane; i < slots; i += 32 * G) {
     const float2 v = __ldcs(part + i);
-    k::ce_combine(c, s, v.x, v.y);
+    join_stats(c, s, v.x, v.y);
   }
   combine_stats<G>(c, s);
 }

@@ -81,3 +81,32 @@ def test_oracle_and_kernel_agree_on_infinite_ratios(V, Vp):
     rest = np.isfinite(rl)
     assert np.all(loss[~rest] == rl[~rest]) and np.all(np.abs(loss - rl)[rest] <= 2.0 ** -23 * np.abs(rl)[rest])
     assert np.all(dz[rest] == rdz[rest]) and loss[1] == np.inf
+
+
+@pytest.mark.parametrize("V,Vp", [(40, 48), (100, 104), (1000, 1024), (9001, 9008), (50257, 50304), (120001, 120008)])
+def test_no_nan_is_lost_from_a_row(V, Vp):
+    """Whole 16-byte pieces of NaN, at all places of two lanes whose sums are joined first."""
+    rng = np.random.default_rng(V)
+    z = rng.standard_normal((4, Vp))
+    lanes = (np.arange(Vp) // 8) % 32
+    t = np.full(4, 3)                                   # a piece of its own
+    z[0, 8:16] = np.nan
+    z[1, (lanes == 5) | (lanes == 21)] = np.nan
+    z[2, (lanes == 5) | (lanes == 21)] = -np.inf
+    z[2, 5 * 8] = np.nan
+    z[:, V:] = 1.0
+    if V < 45:
+        z[2, 8] = np.nan
+    zd, err = bf16(z), err_word()
+    lp = torch.zeros(4, device="cuda")
+    gs.token_logps(zd, i32(t), lp, V, err)
+    want = [True, bool(V > 40) or bool(np.isnan(z[1, :V]).any()), True, False]
+    assert [bool(v) for v in np.isnan(host(lp))] == want
+    for inplace in (False, True):
+        seq, losses = torch.zeros(2, device="cuda"), torch.zeros(1, device="cuda")
+        ws = torch.empty(gs.preference_loss_workspace(4, 1), dtype=torch.uint8, device="cuda")
+        src = zd.clone()
+        dz = src if inplace else torch.zeros_like(zd)
+        gs.preference_loss(src, i32(t), i32([0, 3, 4]), dz, lp, seq, losses, V, ws, err)
+        assert np.isnan(host(seq)[0]) and np.isfinite(host(seq)[1]) and np.isnan(host(losses)[0])
+        assert [bool(v) for v in np.isnan(host(lp))] == want

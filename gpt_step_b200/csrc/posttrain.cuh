@@ -697,7 +697,7 @@ GPT2_DEV float2 pair_of(const PairArgs& a, int p, bool put) {
       // softplus(+-x) and sigma(+-x) from one exponential
       const double x = b * delta, e = exp(-fabs(x)), big = 1.0 / (1.0 + e), small = e * big;
       const double l = put ? log1p(e) : 0.0, up = fmax(-x, 0.0) + l, down = fmax(x, 0.0) + l;   // softplus(-x), softplus(x)
-      loss = (1.0 - eps) * up + eps * down;
+      loss = (1.0 - eps) * up + (eps > 0.0 ? eps * down : 0.0);   // (down may be infinite)
       dd = -b * (x > 0 ? (1.0 - eps) * small - eps * big : (1.0 - eps) * big - eps * small);
     } else {
       const double off = delta - 0.5 / b;

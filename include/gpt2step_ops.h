@@ -221,6 +221,8 @@ int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* 
  * divided by their number; 0 for none) and D = (S_c - ref_c) - (S_r - ref_r),
  *   GPT2_PREFERENCE_SIGMOID  losses = -(1 - smoothing) log sigma(beta D) - smoothing log sigma(-beta D)
  *   GPT2_PREFERENCE_SQUARED  losses = (D - 1 / (2 beta))^2          (smoothing 0)
+ * A token that the model rules out (logit -inf) makes S = -inf and the loss its limit:
+ * without smoothing 0 for a rejected one, +inf for a chosen one.
  * losses fp32 [P], seq_logps fp32 [2P] (may be NULL) = S, logps fp32 [N] = lp;
  * ref_logp fp32 [2P] (NULL: 0). Rows in no sequence are left as they were, in
  * logps and dlogits too. A pair with a bound that is not one gives loss 0, no

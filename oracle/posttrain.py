@@ -65,7 +65,9 @@ def policy_loss(z, targets, V, old, adv, ref=None, weight=None, ignore_index=-1,
 def pair_loss(delta, kind, beta, smoothing):
     """The pair's loss and its derivative by the margin."""
     if kind == "sigmoid":
-        loss = (1 - smoothing) * np.logaddexp(0, -beta * delta) + smoothing * np.logaddexp(0, beta * delta)
+        loss = (1 - smoothing) * np.logaddexp(0, -beta * delta)
+        if smoothing:                                      # (0 of an infinite loss is 0)
+            loss = loss + smoothing * np.logaddexp(0, beta * delta)
         d = -beta * ((1 - smoothing) * np.exp(-np.logaddexp(0, beta * delta))
                      - smoothing * np.exp(-np.logaddexp(0, -beta * delta)))
         return loss, d

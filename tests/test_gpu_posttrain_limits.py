@@ -110,3 +110,33 @@ def test_no_nan_is_lost_from_a_row(V, Vp):
         gs.preference_loss(src, i32(t), i32([0, 3, 4]), dz, lp, seq, losses, V, ws, err)
         assert np.isnan(host(seq)[0]) and np.isfinite(host(seq)[1]) and np.isnan(host(losses)[0])
         assert [bool(v) for v in np.isnan(host(lp))] == want
+
+
+@pytest.mark.parametrize("rows", [1, 5000])             # the coefficient inside the gradient's launch, and in its own
+@pytest.mark.parametrize("V,Vp", [(40, 48), (50257, 50304)])
+def test_preference_loss_of_tokens_that_are_ruled_out(rows, V, Vp):
+    """A token of logit -inf: its sequence's log-probability is -inf, and the losses are their limits."""
+    if rows > 1 and V > 40:
+        rows = 40
+    rng = np.random.default_rng(V + rows)
+    N = 4 * rows
+    z = np.round(rng.standard_normal((N, Vp)) * 4) / 4
+    t = rng.integers(0, V, N)
+    z[rows, t[rows]] = -np.inf                          # pair 0: the rejected sequence; pair 1: the chosen one
+    z[2 * rows, t[2 * rows]] = -np.inf
+    start = np.arange(5) * rows
+    for kind, smoothing, want in (("sigmoid", 0.0, (0.0, np.inf)), ("sigmoid", 0.1, (np.inf, np.inf)),
+                                  ("squared", 0.0, (np.inf, np.inf))):
+        lp, seq = torch.empty(N, device="cuda"), torch.empty(4, device="cuda")
+        losses, err = torch.empty(2, device="cuda"), err_word()
+        dz = torch.full((N, Vp), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(gs.preference_loss_workspace(N, 2), dtype=torch.uint8, device="cuda")
+        gs.preference_loss(bf16(z), i32(t), i32(start), dz, lp, seq, losses, V, ws, err, kind=kind, beta=0.3,
+                           smoothing=smoothing)
+        assert tuple(host(losses)) == want and int(err.sum()) == 0
+        rl, rs, rlp, rdz = PT.preference_loss(z, t, V, start, kind=kind, beta=0.3, smoothing=smoothing)
+        assert tuple(rl) == want
+        assert host(seq)[1] == -np.inf and host(seq)[2] == -np.inf and np.isfinite(host(seq)[[0, 3]]).all()
+        if kind == "sigmoid":                           # slopes -beta (0, or -smoothing's part) and -beta (1 - smoothing)
+            g = np.repeat([0.3 * smoothing, 0.3 * (1 - smoothing)], 2 * rows)
+            assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g))

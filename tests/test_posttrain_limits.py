@@ -22,3 +22,12 @@ def test_a_policy_row_with_a_nan_has_no_loss_and_no_slope():
         assert all(np.isnan(rows(**bad))), bad
     for fine in (dict(old=nan), dict(old=-inf), dict(old=inf), dict(lp=-inf, old=-inf)):
         assert rows(adv=0.0, **fine) == (0.0, 0.0), fine      # an advantage of 0 gives 0 for any ratio
+
+
+def test_a_pair_whose_margin_is_infinite_has_its_limits():
+    delta = np.array([np.inf, -np.inf, 3000.0, -3000.0])
+    loss, d = PT.pair_loss(delta, "sigmoid", 0.5, 0.0)
+    assert loss.tolist() == [0.0, np.inf, 0.0, 1500.0] and d.tolist() == [0.0, -0.5, 0.0, -0.5]
+    loss, d = PT.pair_loss(delta, "sigmoid", 0.5, 0.25)
+    assert loss.tolist() == [np.inf, np.inf, 375.0, 1125.0] and d.tolist() == [0.125, -0.375, 0.125, -0.375]
+    assert np.isnan(PT.pair_loss(np.array([np.nan]), "sigmoid", 0.5, 0.0)[0]).all()

@@ -254,9 +254,9 @@ GPT2_DEV void policy_row(const PolicyArgs& a, float lp, float old_lp, float adv,
   loss = active ? -free_s : -cut_s;
   g = active ? -free_s : 0.f;
   if (a.ref_logp) {
-    // e^d - d - 1 without the cancellation of small d
+    // e^d - d - 1 without the cancellation of small d, and +inf where d is
     const float d = ref - lp, em = expm1f(d);
-    loss += a.kl_coef * (em - d);
+    loss += a.kl_coef * (em - fminf(d, 3.402823466e38f));
     g -= a.kl_coef * em;
   }
   loss *= w;

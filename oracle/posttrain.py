@@ -46,7 +46,8 @@ def policy_rows(lp, old, adv, ref, w, clip_low, clip_high, kl):
     g = np.where(free > cut, 0.0, -free)
     if ref is not None and kl:
         d = ref - lp
-        loss = loss + kl * (np.expm1(d) - d)
+        # e^d grows past d: +inf where d is
+        loss = loss + kl * (np.expm1(d) - np.minimum(d, np.finfo(F64).max))
         g = g - kl * np.expm1(d)
     return w * loss, w * g
 

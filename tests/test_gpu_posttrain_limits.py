@@ -140,3 +140,16 @@ def test_preference_loss_of_tokens_that_are_ruled_out(rows, V, Vp):
         if kind == "sigmoid":                           # slopes -beta (0, or -smoothing's part) and -beta (1 - smoothing)
             g = np.repeat([0.3 * smoothing, 0.3 * (1 - smoothing)], 2 * rows)
             assert np.all(np.abs(host(dz) - rdz) <= grad_tol(rdz, g))
+
+
+@pytest.mark.parametrize("V,Vp", WIDTHS)
+def test_policy_loss_of_a_token_that_only_the_reference_allows(V, Vp):
+    """The policy rules the token out, the reference does not: the KL term is +inf, not a NaN."""
+    _, z, t = rows_case(3, V, Vp, V + 2, masked=0.0)
+    z[1, t[1]] = -np.inf
+    old, adv = np.zeros(3), np.ones(3)
+    ref = np.array([-1.0, -1.0, -np.inf])               # row 2 the other way round: infinite too
+    _, loss, _ = policy(z, t, V, old, adv, ref_logp=ref, kl_coef=0.1)
+    rl = PT.policy_loss(z, t, V, old, adv, ref=ref, kl=0.1)[0]
+    assert loss[1] == np.inf and loss[2] == np.inf and rl[1] == np.inf and rl[2] == np.inf
+    assert math.isfinite(loss[0]) and abs(loss[0] - rl[0]) <= 1e-5 * (1 + abs(rl[0]))

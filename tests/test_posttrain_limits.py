@@ -31,3 +31,9 @@ def test_a_pair_whose_margin_is_infinite_has_its_limits():
     loss, d = PT.pair_loss(delta, "sigmoid", 0.5, 0.25)
     assert loss.tolist() == [np.inf, np.inf, 375.0, 1125.0] and d.tolist() == [0.125, -0.375, 0.125, -0.375]
     assert np.isnan(PT.pair_loss(np.array([np.nan]), "sigmoid", 0.5, 0.0)[0]).all()
+
+
+def test_the_kl_term_of_infinite_log_ratios_is_infinite():
+    assert rows(lp=-np.inf, old=0.0, ref=-1.0) == (np.inf, -np.inf)      # ruled out by the policy alone
+    loss, g = rows(ref=-np.inf)                                          # and by the reference alone
+    assert loss == np.inf and g == -1.0 + 0.1

@@ -528,6 +528,22 @@ __global__ void __launch_bounds__(32 * G) policy_streamed_kernel(const PolicyArg
   else streamed_gradient(zr, dr, t, a.V, a.Vp, c, s, g, threadIdx.x, 32 * G);
 }
 
+// The rows that the sequences cut up: from the first bound to the last, or all where those are no bounds.
+struct RowSpan {
+  long begin, end;
+  GPT2_DEV RowSpan(const int32_t* start, int n_seq, int N) : begin(start[0]), end(start[n_seq]) {
+    if (begin < 0 || end < begin || end > N) {
+      begin = 0;
+      end = N;
+    }
+  }
+  // Pair p's three bounds, and whether they are bounds.
+  GPT2_DEV int4 bounds(const int32_t* start, int p) const {
+    const int32_t a = start[2 * p], b = start[2 * p + 1], c = start[2 * p + 2];
+    return make_int4(a, b, c, begin <= a && a <= b && b <= c && c <= end);
+  }
+};
+
 struct RowArgs {
   const bf16* logits;
   const int32_t* targets;
@@ -535,7 +551,7 @@ struct RowArgs {
   float2* stats;            // (c, S) per row, or null
   const float2* part;
   const float* tgt_val;     // the target's logit per row where the logits are not stored, or null
-  const int32_t* seq_start; // only rows seq_start[0] .. seq_start[n_seq] - 1, or null: all rows
+  const int32_t* seq_start; // only the rows of its span, or null: all rows
   int N, n_seq, slots, V, Vp, ignore_index;
   int* err;
 };
@@ -554,8 +570,9 @@ __global__ void __launch_bounds__(32 * G, 32 / G) row_logp_kernel(const RowArgs 
   RowPipe<G> pipe{row_slots, smem_u32(row_slots), (a.V + 7) / 8, red, 0};
   long begin = 0, end = a.N;
   if (a.seq_start) {
-    begin = a.seq_start[0];
-    end = min(end, (long)a.seq_start[a.n_seq]);
+    const RowSpan span(a.seq_start, a.n_seq, a.N);
+    begin = span.begin;
+    end = span.end;
   }
   RowWindows win(a.targets, a.logits, begin, end, a.V, a.Vp, a.ignore_index);
   auto advance = [&]() {
@@ -599,7 +616,10 @@ template <int G, bool PART>
 __global__ void __launch_bounds__(32 * G) row_logp_streamed_kernel(const RowArgs a) {
   pdl_begin();
   const int row = blockIdx.x;
-  if (a.seq_start && (row < a.seq_start[0] || row >= a.seq_start[a.n_seq])) return;
+  if (a.seq_start) {
+    const RowSpan span(a.seq_start, a.n_seq, a.N);
+    if (row < span.begin || row >= span.end) return;
+  }
   const size_t off = (size_t)row * a.Vp;
   const int t = a.targets[row];
   if (!row_kept(t, a.V, a.ignore_index)) {
@@ -627,7 +647,7 @@ struct PairArgs {
   float* seq_logps;           // [2 P] or null
   float* losses;              // [P]
   float2* coef;               // [P], or null where pair_grad_kernel forms them itself
-  int N, seq_len, V, ignore_index, kind, average;
+  int N, n_pairs, seq_len, V, ignore_index, kind, average;
   float beta, smoothing, dscale;
   int* err;
 };
@@ -650,19 +670,15 @@ GPT2_DEV float2 pair_of(const PairArgs& a, int p, bool put) {
   __shared__ int cnt[2][W];
   __shared__ float2 coef;
   bool bad = false;
+  int4 at{};
+  if (a.seq_start) {
+    at = RowSpan(a.seq_start, 2 * a.n_pairs, a.N).bounds(a.seq_start, p);
+    bad = !at.w;
+    if (bad) at = make_int4(0, 0, 0, 0);
+  }
   for (int h = 0; h < 2; ++h) {
-    long b, e;
-    if (a.seq_start) {
-      b = a.seq_start[2 * p + h];
-      e = a.seq_start[2 * p + h + 1];
-    } else {
-      b = (2L * p + h) * a.seq_len;
-      e = b + a.seq_len;
-    }
-    if (b < 0 || e < b || e > a.N) {
-      bad = true;
-      b = e = 0;
-    }
+    const long b = a.seq_start ? (h ? at.y : at.x) : (2L * p + h) * a.seq_len;
+    const long e = a.seq_start ? (h ? at.z : at.y) : b + a.seq_len;
     double s = 0.0;
     int n = 0;
 #pragma unroll 8
@@ -734,15 +750,21 @@ struct PairGradArgs {
   int N, n_seq, seq_len, V, Vp, ignore_index;
 };
 
-// The sequence that holds `row`, or -1: the last one that begins at or before it.
-GPT2_DEV int find_sequence(const int32_t* start, int n_seq, int row) {
+// The sequence that holds `row`: the last one that begins at or before it. kOutside for rows
+// in front of the first and behind the last, kNone where bounds that are not bounds let none be found.
+constexpr int kOutside = -1, kNone = -2;
+GPT2_DEV int find_sequence(const int32_t* start, int n_seq, int N, int row) {
+  const RowSpan span(start, n_seq, N);
   int lo = 0, hi = n_seq;   // start[lo] <= row is looked for in [0, n_seq)
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (start[mid] <= row) lo = mid + 1;
     else hi = mid;
   }
-  return (lo > 0 && row < start[lo]) ? lo - 1 : -1;
+  if (row < span.begin || row >= span.end) return kOutside;
+  const int s = max(lo - 1, 0);
+  const int4 b = span.bounds(start, s >> 1);
+  return b.w && row >= (s & 1 ? b.y : b.x) && row < (s & 1 ? b.z : b.y) ? s : kNone;
 }
 
 // The rows' gradients from their (c, S): a warp a row where G is 1 (four a CTA), else the
@@ -764,11 +786,11 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const 
   }
   const int w = G == 1 ? threadIdx.x >> 5 : 0, lane = G == 1 ? lane_id() : threadIdx.x;
   const long row = (long)(gridDim.x - 1 - blockIdx.x) * kRows + w;
-  int seq = -1, t = 0;
+  int seq = kOutside, t = 0;
   bool kept = false;
   if (row < a.N) {
-    seq = a.seq_start ? find_sequence(a.seq_start, a.n_seq, (int)row) : (int)(row / a.seq_len);
-    if (seq >= a.n_seq) seq = -1;
+    seq = a.seq_start ? find_sequence(a.seq_start, a.n_seq, a.N, (int)row) : (int)(row / a.seq_len);
+    if (seq >= a.n_seq) seq = kOutside;
     t = a.targets[row];
     kept = seq >= 0 && row_kept(t, a.V, a.ignore_index);
   }
@@ -788,7 +810,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) pair_grad_kernel(const 
     }
     c = coef_s[w];
   }
-  if (seq < 0) return;   // behind the last sequence: left as it was
+  if (seq == kOutside) return;   // left as it was
   const size_t off = (size_t)row * a.Vp;
   uint4* dr = reinterpret_cast<uint4*>(a.dlogits + off);
   if (!kept) {
@@ -895,7 +917,7 @@ inline int row_logps(const RowArgs& a, cudaStream_t s) {
 // 45.9 against 42.1 and 1 of 2 x 8,192 x 1,000 (256 MB) 49 against 29. Rows over 16,384
 // ids take the launch: 2 of 2 x 200 x 30,000 29.0 us against 27.8.
 inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s) {
-  const int P = a.n_seq / 2;
+  const int P = pa.n_pairs = a.n_seq / 2;
   const int rows = a.Vp <= 4608 ? 4 : 1;   // a CTA's
   if (a.dlogits && a.Vp <= 16384 && a.N <= 8192 && (long)a.N * a.N / ((long)P * rows) <= 1 << 20) {
     pa.coef = nullptr;

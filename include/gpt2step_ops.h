@@ -225,8 +225,10 @@ int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* 
  * without smoothing 0 for a rejected one, +inf for a chosen one.
  * losses fp32 [P], seq_logps fp32 [2P] (may be NULL) = S, logps fp32 [N] = lp;
  * ref_logp fp32 [2P] (NULL: 0). Rows in no sequence are left as they were, in
- * logps and dlogits too. A pair with a bound that is not one gives loss 0, no
- * gradient and flag 1. 0 < beta, 0 <= smoothing < 1. The workspace is 8-byte
+ * logps and dlogits too. A bound that is not one (outside [0, N], below the one
+ * before it or above the last) sets flag 1: its pair gives loss 0 and no gradient,
+ * other pairs their losses, but some of their rows may be left without a gradient.
+ * 0 < beta, 0 <= smoothing < 1. The workspace is 8-byte
  * aligned; concurrent calls must not share one. */
 size_t gpt2op_preference_loss_workspace(int N, int P);
 int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int32_t* seq_start, const float* ref_logp,

@@ -153,3 +153,54 @@ def test_policy_loss_of_a_token_that_only_the_reference_allows(V, Vp):
     rl = PT.policy_loss(z, t, V, old, adv, ref=ref, kl=0.1)[0]
     assert loss[1] == np.inf and loss[2] == np.inf and rl[1] == np.inf and rl[2] == np.inf
     assert math.isfinite(loss[0]) and abs(loss[0] - rl[0]) <= 1e-5 * (1 + abs(rl[0]))
+
+
+BAD_BOUNDS = [
+    # bounds, pairs that have theirs
+    ([2000000000, 5, 10, 15, 20], [False, True]),
+    ([-3, 5, 10, 15, 20], [False, True]),
+    ([0, 5, 10, 15, 21], [True, False]),
+    ([0, 5, 9, 4, 20], [True, False]),
+    ([0, 15, 20, 20, 12], [False, False]),      # the first pair ends behind the last bound
+    ([4, 6, 9, 9, 2], [True, False]),          # the last bound before the first: every row may be in a pair
+    ([0, 5, 10, 19, 12, 14, 16], [True, False, True]),
+    ([6, 2, 7, 9, 12, 14, 16], [False, True, True]),
+    ([0, 3, 5, 1000000, -5, 8, 13], [True, False, False]),
+    ([9, 3, 1], [False]),
+]
+
+
+@pytest.mark.parametrize("start,good", BAD_BOUNDS)
+@pytest.mark.parametrize("V,Vp,rows", [(30, 32, 20), (5001, 5008, 20), (20001, 20008, 20), (30, 32, 9000)])
+def test_pairs_beside_bounds_that_are_not_bounds(start, good, V, Vp, rows):
+    """Pairs of sound bounds get their loss, and their rows their gradient or none; the others 0 and none; flag 1."""
+    _, z, t = rows_case(rows, V, Vp, 8, masked=0.2)
+    start, P = np.array(start), len(good)
+    err, losses = err_word(), torch.full((P,), 9.0, device="cuda")
+    dz = torch.full((rows, Vp), 5.0, dtype=torch.bfloat16, device="cuda")
+    logps = torch.full((rows,), float("nan"), device="cuda")
+    ws = torch.full((gs.preference_loss_workspace(rows, P),), 0xFF, dtype=torch.uint8, device="cuda")
+    if rows > 20:
+        start = np.where(start == 20, rows, np.where(start == 21, rows + 1, start))
+    gs.preference_loss(bf16(z), i32(t), i32(start), dz, logps, None, losses, V, ws, err, beta=0.5, dscale=1.0)
+    assert int(err[0]) == 1
+    got, covered = host(dz), np.zeros(rows, bool)
+    for p in range(P):
+        if not good[p]:
+            assert float(losses[p]) == 0.0
+            continue
+        b = start[2 * p:2 * p + 3]
+        rl, _, rlp, rdz = PT.preference_loss(z, t, V, b, beta=0.5)
+        tol = (b[2] - b[0]) * lp_tol(np.abs(rlp).max())
+        assert abs(float(losses[p]) - rl[0]) <= 0.5 * tol + 2.0 ** -22 * abs(rl[0])
+        in_pair = slice(b[0], b[2])
+        g = np.full(rows, 0.5)
+        # (the slope's change over the margin's error: beta^2 / 4 of it); the search may miss a row's sequence
+        right = np.all(np.abs(got - rdz) <= grad_tol(rdz, g) + 0.07 * tol, axis=1)
+        none = np.all(got == 0, axis=1)
+        assert np.all((right | none)[in_pair])
+        if len(good) < 3:
+            assert np.all(right[in_pair])
+        covered[in_pair] = True
+    rest = got[~covered]
+    assert np.all((rest == 0) | (rest == 5.0)) and np.all(rest.min(1) == rest.max(1))

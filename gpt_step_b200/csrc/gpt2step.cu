@@ -579,8 +579,7 @@ int spec_loss(gpt2_model* m, const LossSpec& spec, const int32_t* tgt, int N, bf
       g.logits = g.dlogits = logits;
       g.targets = tgt; g.stats = stats; g.n_seq = 2 * P; g.seq_len = d.T; g.V = d.V; g.Vp = d.Vp;
       g.ignore_index = spec.ignore_index; g.N = N;
-      GPT2_TRY(pt::pairs(g, a, stats + d.N, s));
-      nl += 2;
+      GPT2_TRY(pt::pairs(g, a, stats + d.N, s, &nl));
       n_loss = P;
       loss_src = a.losses;
       factor = a.dscale;

@@ -916,15 +916,17 @@ inline int row_logps(const RowArgs& a, cudaStream_t s) {
 // against 19.3, 16 of 2 x 128 x 1,000 13.8 either way; above, 8 of 2 x 512 x 4,353 (8 MB)
 // 45.9 against 42.1 and 1 of 2 x 8,192 x 1,000 (256 MB) 49 against 29. Rows over 16,384
 // ids take the launch: 2 of 2 x 200 x 30,000 29.0 us against 27.8.
-inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s) {
+inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s, int* launches = nullptr) {
   const int P = pa.n_pairs = a.n_seq / 2;
   const int rows = a.Vp <= 4608 ? 4 : 1;   // a CTA's
   if (a.dlogits && a.Vp <= 16384 && a.N <= 8192 && (long)a.N * a.N / ((long)P * rows) <= 1 << 20) {
+    if (launches) *launches += 1;
     pa.coef = nullptr;
     return rows == 4
                ? launched(launch_pdl(pair_grad_kernel<1, true>, dim3(P + (a.N + 3) / 4), dim3(128), 0, s, a, pa))
                : launched(launch_pdl(pair_grad_kernel<4, true>, dim3(P + a.N), dim3(128), 0, s, a, pa));
   }
+  if (launches) *launches += a.dlogits ? 2 : 1;
   pa.coef = coef;
   const int st = launched(launch_pdl(pair_kernel, dim3(P), dim3(kPairThreads), 0, s, pa));
   if (st != GPT2_OK || !a.dlogits) return st;

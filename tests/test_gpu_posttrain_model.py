@@ -146,3 +146,34 @@ def test_preference_gradient_is_that_of_its_rows(B, V, average):
     adv = (-per)[:, None].expand(B, m.T).float().contiguous()
     pol = grads_of(m, lambda: m.fwd_bwd_policy(xt, yt, lp, adv))
     check_same(pref, pol)
+
+
+def launches_of(m, run):
+    before = m.kernel_launches()
+    run()
+    return m.kernel_launches() - before
+
+
+def device_launches(run):
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+        run()
+        torch.cuda.synchronize()
+    return sum(1 for e in prof.events() if e.device_type == torch.autograd.DeviceType.CUDA
+               and not e.name.lower().startswith("mem"))
+
+
+# B, T, V and the launches behind the rows' log-probabilities: the pairs in the gradient's launch, or a launch before it
+@pytest.mark.parametrize("B,T,V,pair_launches", [(4, 64, 1000, 1), (2, 64, 20001, 2), (4, 64, 50257, 2), (10, 1024, 300, 2)])
+def test_launch_count_of_the_preference_micro_step(B, T, V, pair_launches):
+    m = model(B, V, seq_len=T, n_layer=1)
+    _, x, y = batch(m, V, 4)
+    xt, yt = i32(x), i32(y)
+    one = torch.ones(B, T, device="cuda")
+    # the policy micro-step differs by one launch for the rows in place of two or three
+    policy = launches_of(m, lambda: m.fwd_bwd_policy(xt, yt, one, one))
+    pref = launches_of(m, lambda: m.fwd_bwd_preference(xt, yt))
+    assert pref - policy == pair_launches
+    made = [device_launches(lambda: m.fwd_bwd_policy(xt, yt, one, one)),
+            device_launches(lambda: m.fwd_bwd_preference(xt, yt))]
+    if made[0]:                                             # (0 where the profiler has no access to the device)
+        assert made[1] - made[0] == pair_launches

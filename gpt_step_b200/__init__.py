@@ -270,6 +270,7 @@ class GPT2:
         self.T = cfg.seq_len
         self.B = cfg.micro_batch
         self._infos = None
+        self.sharded = False     # set by the sharded data-parallel step: a rank's update is its shards' alone
 
     def close(self):
         if getattr(self, "h", None):
@@ -327,7 +328,11 @@ class GPT2:
 
     def clip_muon(self, step: int, workspace, momentum: float = 0.95, want_norm: bool = False):
         """The optimizer step with orthogonalised momentum for the blocks' 2-D weights;
-        workspace: a device tensor of at least muon_workspace(cfg) bytes."""
+        workspace: a device tensor of at least muon_workspace(cfg) bytes. On several ranks with
+        DataParallel(mode="allreduce"): sync_grads(), then this; the sharded form cuts through matrices."""
+        if self.sharded:
+            raise ValueError("clip_muon: the model's update is sharded over ranks, which cuts through matrices "
+                             "(DataParallel(mode=\"allreduce\") keeps them whole)")
         out = ctypes.c_float()
         ws = _need(workspace, "workspace", _types()[3], -1, self.arena.get_device())
         check(lib().gpt2_clip_muon(self.h, step, momentum, ws, workspace.numel(),

@@ -55,6 +55,8 @@ class DataParallel:
         self.comm = None
         if mode == "zero1":
             self._setup_zero1()
+        # whole-matrix updates (clip_muon) are refused where a rank's gradients and masters are its shards' alone
+        model.sharded = mode == "zero1" and self.world > 1
 
     # -- helpers ------------------------------------------------------------------------------
     def _stream(self):

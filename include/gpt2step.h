@@ -274,7 +274,8 @@ int gpt2_fwd_bwd_preference(gpt2_model* model, const int32_t* tokens_dev, const 
  * mean square of AdamW's, so that one schedule serves both. GPT2_ADAM_V of those
  * weights is left alone. 0 <= momentum < 1. workspace: device memory of at least
  * gpt2_muon_workspace(cfg) bytes, 256-byte aligned. Not for the sharded step,
- * whose shards cut through matrices. */
+ * whose shards cut through matrices (this call does not see it; the Python class
+ * refuses): on several ranks average the whole gradient array first. */
 size_t gpt2_muon_workspace(const gpt2_config* cfg);
 int gpt2_clip_muon(gpt2_model* model, int32_t step, float momentum, void* workspace, size_t ws_bytes,
                    float* grad_norm_out);

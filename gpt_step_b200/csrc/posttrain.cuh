@@ -909,17 +909,25 @@ inline int row_logps(const RowArgs& a, cudaStream_t s) {
 }
 
 // What follows the rows' log-probabilities: the pairs' losses, and with a.dlogits the
-// gradients. A pair's coefficient is formed in the gradient's launch while that reads no
-// more than 4 MB (pairs of like length; the bound on the rows is for one pair that has
-// nearly all of them), a launch of its own otherwise. Pairs of 2 x 64 x 1,000 11.7 us a
-// call against 13.8, 1 of 2 x 1,024 x 1,000 15.8 against 20.2, 4 of 2 x 512 x 1,000 15.7
-// against 19.3, 16 of 2 x 128 x 1,000 13.8 either way; above, 8 of 2 x 512 x 4,353 (8 MB)
-// 45.9 against 42.1 and 1 of 2 x 8,192 x 1,000 (256 MB) 49 against 29. Rows over 16,384
-// ids take the launch: 2 of 2 x 200 x 30,000 29.0 us against 27.8.
+// gradients. Times of a whole call on the device (captured), and from the host one by one.
+//
+// A row a warp where rows are many and short, else a row a CTA. 512 rows of 1,024 ids 7.8 us
+// against 6.7, 1,024 of 2,048 11.0 against 9.5; 1,536 of 2,048 11.8 against 12.9, 4,096 of
+// 4,608 25.2 against 28.9; the long end of the rule: 1,536 of 6,144 19.4 against 18.5, 2,048
+// of 6,144 21.0 either way, 4,096 of 8,192 37.7 against 39.0, 8,192 of 12,288 107 against 106.
+//
+// A pair's coefficient is formed in the gradient's launch where N rows add up no more than
+// 8 MB of log-probabilities however the pairs divide them (all in one pair: N / rows CTAs
+// times N), a launch of its own otherwise. From the host a launch costs 2 us: 256 rows of
+// 1,000 ids 11.6 us against 13.6, 1,206 of 8,449 17.8 against 19.0; on the device 1,536 of 2,048 11.8 us
+// against 12.6, and above the bound 4,096 of 1,024 13.4 against 12.0, with nearly all rows in
+// one of 4 pairs 16.1 against 13.5 (8,192 of 5,120, 256 MB: 79 against 61). A row a warp and
+// longer rows take the launch (2,048 of 4,608 22.3 against 18.4), as do rows over 16,384 ids
+// (2 of 2 x 200 x 30,000 29.0 against 27.8).
 inline int pairs(PairGradArgs a, PairArgs pa, float2* coef, cudaStream_t s, int* launches = nullptr) {
   const int P = pa.n_pairs = a.n_seq / 2;
-  const int rows = a.Vp <= 4608 ? 4 : 1;   // a CTA's
-  if (a.dlogits && a.Vp <= 16384 && a.N <= 8192 && (long)a.N * a.N / ((long)P * rows) <= 1 << 20) {
+  const int rows = a.N > 1024 && a.Vp <= std::min(3L * a.N, 10240L) ? 4 : 1;   // a CTA's
+  if (a.dlogits && a.Vp <= (rows == 4 ? 2048 : 16384) && (long)a.N * a.N / rows <= 1 << 21) {
     if (launches) *launches += 1;
     pa.coef = nullptr;
     return rows == 4

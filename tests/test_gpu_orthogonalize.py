@@ -123,3 +123,77 @@ def test_accuracy_is_that_of_the_documented_roundings(b, r, c, steps):
         got = run(x, steps)
         for i in range(min(b, len(kinds))):
             check(got[i], x[i], steps)
+
+
+@pytest.mark.parametrize("r,c", [(150, 220), (301, 700), (700, 301)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4])
+def test_accuracy_of_few_steps(r, c, steps):
+    """Where the second half of X is carried through no, or one, round."""
+    x = torch.stack([matrix(r, c, k, steps) for k in SPECTRA]).float()
+    got = run(x, steps)
+    for g, m in zip(got, x):
+        check(g, m, steps)
+
+
+# matrices that go through memory: tall and wide, rows that are no whole 16 bytes, tiles of both widths, few columns
+LAYOUTS = [(2, 517, 333), (1, 701, 301), (2, 333, 517), (40, 300, 257), (40, 257, 300), (80, 131, 2050), (1, 2100, 130),
+           (3, 2100, 24), (3, 24, 2100), (2, 2049, 9)]
+
+
+def layouts(b, r, c, dt, gap_x, gap_o, off_x, off_o):
+    """x and out inside larger buffers: matrices gap elements apart, the first off elements in."""
+    n = r * c
+    xb = torch.full((off_x + b * (n + gap_x),), 3.0, dtype=dt, device="cuda")
+    ob = torch.full((off_o + b * (n + gap_o),), 4.0, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(xb, (b, r, c), (n + gap_x, c, 1), off_x)
+    o = torch.as_strided(ob, (b, r, c), (n + gap_o, c, 1), off_o)
+    return x, o, ob
+
+
+@pytest.mark.parametrize("b,r,c", LAYOUTS)
+@pytest.mark.parametrize("fp32", [True, False])
+@pytest.mark.parametrize("gap_x,gap_o,off_x,off_o", [(0, 0, 0, 0), (64, 8, 16, 8), (7, 5, 3, 1), (8, 3, 0, 0)])
+def test_layouts_of_larger_matrices(b, r, c, fp32, gap_x, gap_o, off_x, off_o):
+    """Against the definition, in any layout the same bits, and nothing written beside a result."""
+    kinds = list(SPECTRA)
+    some = [matrix(r, c, kinds[i % 4], r * c + i).float() for i in range(min(b, 4))]
+    x, o, ob = layouts(b, r, c, torch.float32 if fp32 else torch.bfloat16, gap_x, gap_o, off_x, off_o)
+    for i in range(b):
+        x[i] = some[i % 4]
+    given = x.clone()
+    run(x, out=o)
+    assert torch.equal(x, given)
+    if min(r, c) >= 100:
+        for i in range(min(b, 4)):
+            check(o[i], x[i], 5)
+    else:
+        for i in range(min(b, 4)):
+            # few singular values: the half steps may add up (2^-11 each, three in a round, grown to 36 in all)
+            assert off(o[i], defined(x[i], 5)) <= 2.2e-2
+    assert torch.equal(o, run(given.contiguous()))
+    n = r * c
+    ob[off_o:].view(b, n + gap_o)[:, :n] = 4.0
+    assert bool((ob == 4.0).all())
+
+
+@pytest.mark.parametrize("r,c", [(150, 220), (220, 150), (513, 300), (300, 520)])
+@pytest.mark.parametrize("fp32", [True, False])
+@pytest.mark.parametrize("many", [1, 8])
+def test_zeros_and_non_finite_larger_matrices(r, c, fp32, many):
+    """Each matrix by itself: zeros stay zeros, a NaN or an infinity makes its own matrix NaN, scale does not count."""
+    base = matrix(r, c, "1/k", 7).float()
+    x = torch.stack([base] * 7)
+    x[1] = 0.0
+    x[2, 3, 4] = float("nan")
+    x[3, r - 1, c - 1] = float("inf")
+    x[4] *= 2.0 ** 90
+    x[5] *= 2.0 ** -20
+    x = x.repeat(many, 1, 1)
+    x = x if fp32 else x.to(torch.bfloat16)
+    got = run(x).view(many, 7, r, c)
+    assert bool((got[:, 1] == 0).all()) and bool(torch.isnan(got[:, 2]).all()) and bool(torch.isnan(got[:, 3]).all())
+    for i in (0, 4, 6):
+        check(got[0, i], x[i], 5)
+    check(got[0, 5], x[5], 5)
+    assert all(torch.equal(got[k, i], got[0, i]) for k in range(many) for i in (0, 4, 5, 6))
+    assert torch.equal(got[0, 0], got[0, 6])

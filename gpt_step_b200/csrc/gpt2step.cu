@@ -672,7 +672,7 @@ int forward(gpt2_model* m, const int32_t* tok, const int32_t* tgt, int b, bool t
   // cross-entropy reads the logits once; for a loss alone (evaluation) it keeps
   // only the partials and the target logit, and the logits are never stored
   float2* lse_part = nullptr;
-  bool logits_free = false;
+  float* tgt_val = nullptr;   // where no logits are stored: the targets' (scratch of the backward for a loss of `spec`)
   {
     gemm::Call c = gemm_call(gemm::FWD, gemm::EPI_STORE, (int)N, d.Vp, C, err);
     c.a = lnf; c.lda = C; c.b = m->W(K_WTE); c.ldb = C; c.out = logits; c.ldo = d.Vp;
@@ -680,18 +680,18 @@ int forward(gpt2_model* m, const int32_t* tok, const int32_t* tgt, int b, bool t
       lse_part = m->at<float2>(y.lse_part);
       c.epi = gemm::EPI_LSE; c.lse_part = lse_part; c.lse_V = d.V;
       if (!train) {
-        c.epi = gemm::EPI_LSE_ONLY; c.lse_tgt = tgt; c.lse_tgt_val = losses;
-        logits_free = true;
+        tgt_val = spec ? m->at<float>(y.attD) : losses;
+        c.epi = gemm::EPI_LSE_ONLY; c.lse_tgt = tgt; c.lse_tgt_val = tgt_val;
       }
     }
     GPT2_TRY(run_gemm(m, c));
   }
-  if (spec) return spec_loss(m, *spec, tgt, (int)N, logits, lse_part, logits_free ? losses : nullptr, loss_acc);
+  if (spec) return spec_loss(m, *spec, tgt, (int)N, logits, lse_part, tgt_val, loss_acc);
   {
     const size_t p = prof_begin(m);
-    GPT2_TRY(launch::softmax_ce(logits_free ? nullptr : logits, tgt, losses, (int)N, d.V, d.Vp, 1.0f / (float)N,
+    GPT2_TRY(launch::softmax_ce(tgt_val ? nullptr : logits, tgt, losses, (int)N, d.V, d.Vp, 1.0f / (float)N,
                                 train ? 1 : 0, err, s, INT_MIN, lse_part, lse_slots(d.Vp),
-                                logits_free ? losses : nullptr));
+                                tgt_val));
     launch_pdl(k::loss_reduce_kernel, dim3(1), dim3(1024), 0, s, losses, (int)N, loss_acc, &m->sc()->micro_loss);
     // algorithmic bytes: the logits read (and overwritten when training), or with
     // the GEMM's partials those plus the partials, and no row scan for a loss alone

@@ -236,7 +236,8 @@ int gpt2_clip_adamw_ranges(gpt2_model* model, int32_t step, const int64_t* range
 /* Log-probabilities of the targets under the model: forward only, asynchronous.
  * tokens_dev / targets_dev int32 [batch, seq_len] (batch may exceed micro_batch),
  * logps_dev fp32 [batch, seq_len], 0 where the target is ignore_index. They are
- * the old and reference log-probabilities that the calls below take. */
+ * the old and reference log-probabilities that the calls below take.
+ * gpt2_token_losses still returns the last micro-step's values after it. */
 int gpt2_token_logps(gpt2_model* model, const int32_t* tokens_dev, const int32_t* targets_dev, int32_t batch,
                      int32_t ignore_index, float* logps_dev);
 

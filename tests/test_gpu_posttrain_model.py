@@ -148,6 +148,20 @@ def test_preference_gradient_is_that_of_its_rows(B, V, average):
     check_same(pref, pol)
 
 
+@pytest.mark.parametrize("B,V", SIZES)
+def test_log_probabilities_leave_the_micro_steps_results(B, V):
+    m = model(B, V)
+    _, x, y = batch(m, V, 5)
+    xt, yt = i32(x), i32(y)
+    m.fwd_bwd(xt, yt)
+    losses, grads = m.token_losses(), m.state_tensor(gs.GPT2_GRADS).clone()
+    m.token_logps(i32(x[:, ::-1].copy()), yt, torch.empty(B, m.T, device="cuda"))
+    assert np.array_equal(m.token_losses(), losses)
+    assert torch.equal(m.state_tensor(gs.GPT2_GRADS), grads)
+    m.clip_adamw(0)
+    assert abs(m.last_step_stats()[0] - losses.mean()) <= 1e-5
+
+
 def launches_of(m, run):
     before = m.kernel_launches()
     run()

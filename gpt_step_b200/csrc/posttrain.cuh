@@ -512,13 +512,16 @@ __global__ void __launch_bounds__(32 * G) policy_streamed_kernel(const PolicyArg
     if (dr) zero_row(dr, 0, a.Vp, threadIdx.x, 32 * G);
     return;
   }
-  const float zt = __bfloat162float(a.logits[off + t]);   // before any thread may overwrite it
+  // read by all threads before (the sums' barrier) one of them writes: the logits, and the
+  // inputs if an output takes their place
+  const float zt = __bfloat162float(a.logits[off + t]);
+  const float old_lp = a.old_logp[row], adv = a.adv[row];
+  const float ref = a.ref_logp ? a.ref_logp[row] : 0.f, w = a.weight ? a.weight[row] : 1.f;
   float c, s, loss, g;
   if (PART) part_stats<G>(a.part + (size_t)row * a.slots, a.slots, threadIdx.x, c, s);
   else streamed_stats<G>(zr, a.V, c, s);
   const float lp = row_logp(zt, c, s);
-  policy_row(a, lp, a.old_logp[row], a.adv[row], a.ref_logp ? a.ref_logp[row] : 0.f, a.weight ? a.weight[row] : 1.f,
-             loss, g);
+  policy_row(a, lp, old_lp, adv, ref, w, loss, g);
   if (threadIdx.x == 0) {
     a.losses[row] = loss;
     if (a.logps) a.logps[row] = lp;

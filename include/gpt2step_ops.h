@@ -208,7 +208,8 @@ int gpt2op_token_logps(const void* logits, const int32_t* targets, float* logps,
  *   dlosses/dlp = weight * ( -[r A <= clip(r) A] r A + kl_coef * (1 - e^d) ).
  * An advantage A of 0 gives 0 for any r; any other NaN, of a kept row's logits or
  * inputs, is a NaN in its loss and gradient. old_logp, adv, weight (NULL: 1), ref_logp
- * (NULL with kl_coef 0) fp32 [N]; logps (may be NULL) and losses fp32 [N].
+ * (NULL with kl_coef 0) fp32 [N]; logps (may be NULL) and losses fp32 [N], which may
+ * each take the place of one of the inputs.
  * 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, all finite. */
 int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* old_logp, const float* ref_logp,
                        const float* adv, const float* weight, void* dlogits, float* logps, float* losses, int N, int V,

@@ -204,3 +204,23 @@ def test_pairs_beside_bounds_that_are_not_bounds(start, good, V, Vp, rows):
         covered[in_pair] = True
     rest = got[~covered]
     assert np.all((rest == 0) | (rest == 5.0)) and np.all(rest.min(1) == rest.max(1))
+
+
+@pytest.mark.parametrize("V,Vp", WIDTHS)
+def test_policy_loss_with_outputs_in_the_inputs_place(V, Vp):
+    """logps over old_logp (or the reference), losses over the advantages (or weights)."""
+    rng, z, t = rows_case(400, V, Vp, V + 3)
+    zd, td, err = bf16(z), i32(t), err_word()
+    ins = [f32(-1 - 3 * rng.random(400)), f32(rng.standard_normal(400)), f32(-1 - 3 * rng.random(400)),
+           f32(rng.uniform(0.5, 2, 400))]
+
+    def call(old, adv, ref, w, logps, losses, dz):
+        gs.policy_loss(zd, td, old, adv, dz, logps, losses, V, err, ref_logp=ref, weight=w, kl_coef=0.2)
+        return [v.clone() for v in (logps, losses, dz)]
+
+    want = call(*ins, torch.empty(400, device="cuda"), torch.empty(400, device="cuda"), torch.empty_like(zd))
+    for lp_at, loss_at in ((0, 1), (2, 3), (1, 0), (3, 2)):
+        for _ in range(3):
+            c = [v.clone() for v in ins]
+            got = call(*c, c[lp_at], c[loss_at], torch.empty_like(zd))
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (lp_at, loss_at)

@@ -162,6 +162,26 @@ def test_log_probabilities_leave_the_micro_steps_results(B, V):
     assert abs(m.last_step_stats()[0] - losses.mean()) <= 1e-5
 
 
+@pytest.mark.parametrize("B,V", SIZES)
+def test_policy_micro_step_with_log_probabilities_over_the_old_ones(B, V):
+    m = model(B, V)
+    spread(m)
+    rng, x, y = batch(m, V, 6)
+    xt, yt = i32(x), i32(y)
+    old = torch.empty(B, m.T, device="cuda")
+    m.token_logps(xt, yt, old)
+    old -= f32(0.1 * rng.standard_normal((B, m.T)))
+    adv, lp = f32(rng.standard_normal((B, m.T))), torch.empty_like(old)
+    want = grads_of(m, lambda: m.fwd_bwd_policy(xt, yt, old, adv, logps=lp))
+    losses = m.token_losses()
+    for _ in range(3):
+        over = old.clone()
+        got = grads_of(m, lambda: m.fwd_bwd_policy(xt, yt, over, adv, logps=over))
+        assert torch.equal(over, lp) and np.array_equal(m.token_losses(), losses)
+        # (the gradients' atomics add in any order)
+        check_same(got, want, tol=1e-5)
+
+
 def launches_of(m, run):
     before = m.kernel_launches()
     run()

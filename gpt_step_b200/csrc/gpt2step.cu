@@ -1046,6 +1046,9 @@ static bool policy_scalars(const float* ref_logp, float clip_low, float clip_hig
   return true;
 }
 
+// Whether two arrays of n floats and k floats have no element in common (null: none).
+static bool apart(const float* a, size_t n, const float* b, size_t k) { return !a || !b || a + n <= b || b + k <= a; }
+
 static bool pair_scalars(int kind, int average, float beta, float smoothing, float scale, pt::PairArgs* a) {
   if (kind != GPT2_PREFERENCE_SIGMOID && kind != GPT2_PREFERENCE_SQUARED) return false;
   if (!(beta > 0.f && isfinite(beta)) || !(smoothing >= 0.f && smoothing < 1.f) || !isfinite(scale)) return false;
@@ -1087,7 +1090,7 @@ int gpt2_fwd_bwd_preference(gpt2_model* m, const int32_t* tokens, const int32_t*
                             int32_t ignore_index, int kind, int average, float beta, float smoothing,
                             float* seq_logps, float* loss_out) {
   LossSpec spec{};
-  if (!m || !tokens || !targets || (m->lay.d.B & 1) ||
+  if (!m || !tokens || !targets || (m->lay.d.B & 1) || !apart(ref_logp, m->lay.d.B, seq_logps, m->lay.d.B) ||
       !pair_scalars(kind, average, beta, smoothing, 2.0f / (float)m->lay.d.B, &spec.pair))
     return GPT2_ERR_ARG;
   spec.kind = LossSpec::PREFERENCE;
@@ -1688,6 +1691,10 @@ int gpt2op_preference_loss(const void* logits, const int32_t* targets, const int
   if (!logits || !targets || !seq_start || !logps || !losses || !workspace || !dev_err || P <= 0 || P > (1 << 29) ||
       !pt::logits_ok(logits, N, V, Vp) || !dlogits_ok(logits, dlogits, N, Vp) ||
       !pair_scalars(kind, average, beta, smoothing, dscale, &a))
+    return GPT2_ERR_ARG;
+  // many CTAs read a pair's reference while one writes its outputs
+  if (!apart(ref_logp, 2 * (size_t)P, seq_logps, 2 * (size_t)P) || !apart(ref_logp, 2 * (size_t)P, losses, P) ||
+      !apart(ref_logp, 2 * (size_t)P, logps, N))
     return GPT2_ERR_ARG;
   if (ws_bytes < pt::preference_workspace(N, P) || (reinterpret_cast<uintptr_t>(workspace) & 7)) return GPT2_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

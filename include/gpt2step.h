@@ -258,7 +258,7 @@ int gpt2_fwd_bwd_policy(gpt2_model* model, const int32_t* tokens_dev, const int3
  * are pair p's chosen and rejected ones. ref_logp_dev fp32 [micro_batch]: the
  * reference's log-probability of each sequence (summed, or with `average` mean,
  * over its kept positions), NULL for none; seq_logps_dev fp32 [micro_batch] (may
- * be NULL) receives the model's. gpt2_token_losses then returns the positions'
+ * be NULL, not over ref_logp_dev) receives the model's. gpt2_token_losses then returns the positions'
  * log-probabilities. */
 int gpt2_fwd_bwd_preference(gpt2_model* model, const int32_t* tokens_dev, const int32_t* targets_dev,
                             const float* ref_logp_dev, int32_t ignore_index, int kind, int average, float beta,

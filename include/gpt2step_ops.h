@@ -225,7 +225,7 @@ int gpt2op_policy_loss(const void* logits, const int32_t* targets, const float* 
  * A token that the model rules out (logit -inf) makes S = -inf and the loss its limit:
  * without smoothing 0 for a rejected one, +inf for a chosen one.
  * losses fp32 [P], seq_logps fp32 [2P] (may be NULL) = S, logps fp32 [N] = lp;
- * ref_logp fp32 [2P] (NULL: 0). Rows in no sequence are left as they were, in
+ * ref_logp fp32 [2P] (NULL: 0; refused where an output lies over it). Rows in no sequence are left as they were, in
  * logps and dlogits too. A bound that is not one (outside [0, N], below the one
  * before it or above the last) sets flag 1: its pair gives loss 0 and no gradient,
  * other pairs their losses, but some of their rows may be left without a gradient.

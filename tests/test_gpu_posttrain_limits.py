@@ -224,3 +224,21 @@ def test_policy_loss_with_outputs_in_the_inputs_place(V, Vp):
             c = [v.clone() for v in ins]
             got = call(*c, c[lp_at], c[loss_at], torch.empty_like(zd))
             assert all(torch.equal(a, b) for a, b in zip(got, want)), (lp_at, loss_at)
+
+
+def test_preference_loss_beside_its_reference():
+    """One buffer may hold the reference and the outputs side by side, but not over it."""
+    rng, z, t = rows_case(40, 100, 104, 9)
+    start = i32([0, 10, 20, 30, 40])
+    one = torch.zeros(4 + 4 + 2 + 40, device="cuda")
+    ref, seq, losses, logps = one[:4], one[4:8], one[8:10], one[10:]
+    ws, err = torch.empty(gs.preference_loss_workspace(40, 2), dtype=torch.uint8, device="cuda"), err_word()
+    gs.preference_loss(bf16(z), i32(t), start, None, logps, seq, losses, 100, ws, err, ref_logp=ref)
+    rl, rs, rlp, _ = PT.preference_loss(z, t, 100, host(start).astype(int), ref=np.zeros(4))
+    assert np.all(np.abs(host(logps) - rlp) <= lp_tol(rlp)) and np.allclose(host(losses), rl, atol=1e-4)
+    for over in (dict(seq=ref), dict(losses=ref[1:3]), dict(seq=one[3:7]), dict(seq=None, logps=one[3:43])):
+        a = dict(seq=seq, losses=losses, logps=logps)
+        a.update(over)
+        with pytest.raises(gs.GPT2Error):
+            gs.preference_loss(bf16(z), i32(t), start, None, a["logps"], a["seq"], a["losses"], 100, ws, err, ref_logp=ref)
+    assert np.all(host(ref) == 0)

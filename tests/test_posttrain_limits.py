@@ -1,6 +1,10 @@
 """The post-training definitions where numbers end, on the CPU."""
+import ctypes
+
 import numpy as np
 
+import gpt_step_b200 as gs
+from gpt_step_b200 import build
 from oracle import posttrain as PT
 
 
@@ -37,3 +41,19 @@ def test_the_kl_term_of_infinite_log_ratios_is_infinite():
     assert rows(lp=-np.inf, old=0.0, ref=-1.0) == (np.inf, -np.inf)      # ruled out by the policy alone
     loss, g = rows(ref=-np.inf)                                          # and by the reference alone
     assert loss == np.inf and g == -1.0 + 0.1
+
+
+def test_preference_loss_refuses_outputs_over_the_reference():
+    """Arguments are checked before any is read: the pointers stand for device memory."""
+    build.build()
+    at = lambda k: ctypes.c_void_p(4096 + 4 * k)  # noqa: E731  float k of one buffer
+    far, F = ctypes.c_void_p(1 << 20), ctypes.c_float
+
+    def pref(ref, logps, seq, losses, N=40, P=4):
+        return gs.lib().gpt2op_preference_loss(far, far, far, ref, None, logps, seq, losses, N, P, 100, 104, -1, 0, 0,
+                                               F(0.1), F(0.0), F(1.0), far, 40 * 8 + 4 * 8, far, None)
+    for bad in (dict(seq=at(0)), dict(seq=at(7)), dict(losses=at(7)), dict(losses=at(-3)), dict(logps=at(7)),
+                dict(logps=at(-39))):
+        args = dict(ref=at(0), logps=far, seq=None, losses=far)
+        args.update(bad)
+        assert pref(**args) == 1, bad

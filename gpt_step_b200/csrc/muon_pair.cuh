@@ -17,8 +17,10 @@
 // rounding P near 0.7 costs less than rounding P - a I near -2.8, and the last product then
 // reads nothing but lo.
 //
-// What bounds it: large matrices the tensor pipe under the power limit (16 x 1,536 x 6,144:
-// 4.36 to 4.40 ms, 0.86 PFLOP/s of the products with symmetric ones counted half); 768 rows the
+// What bounds it: large matrices the tensor pipe, not all of the time (16 x 1,536 x 6,144:
+// 4.36 to 4.5 ms, 0.86 PFLOP/s of the products with symmetric ones counted half, 0.62 of what a
+// GEMM sustains under the power limit; diagonal tiles computed whole are 6% of it, the rest has
+// not been taken apart); 768 rows the
 // shared memory, whose bandwidth the operands take whole at the full tensor rate (64 bytes a
 // clock in and out) and an APPLY tile's hi, lo and aux boxes half as much again (tile 6.4 us
 // against 4.5 of main loop; 12 x 2,304 x 768: 458 us); small ones the

@@ -59,3 +59,30 @@ def test_preference_loss_in_every_form(N, V, Vp, skew, average):
     gerr[inside] = np.repeat(beta ** 2 / 4 * np.repeat(dtol, 2) / n, lens)
     assert np.all((np.abs(got - rdz) <= grad_tol(rdz, g) + gerr[:, None])[inside])
     assert np.all(got[~inside] == 5.0) and np.all(got[inside][:, V:] == 0)
+
+
+def test_rows_past_two_to_the_31_elements():
+    """The last rows of 44,000 x 50,304 logits give what they give by themselves, to the bit."""
+    N, V, Vp, n = 44000, 50257, 50304, 300
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.empty(N, Vp, dtype=torch.bfloat16, device="cuda").normal_(0.0, 2.0, generator=gen)
+    t = torch.randint(0, V, (N,), dtype=torch.int32, device="cuda", generator=gen)
+    old = torch.full((N,), -11.0, device="cuda")
+    adv = torch.randn(N, device="cuda", generator=gen)
+    logps, losses, err = torch.empty(N, device="cuda"), torch.empty(N, device="cuda"), err_word()
+    dz = torch.full_like(z, 3.0)
+    last = slice(N - n, N)
+    lp1, ls1, dz1 = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(z[last])
+    gs.policy_loss(z, t, old, adv, dz, logps, losses, V, err)
+    gs.policy_loss(z[last], t[last], old[last], adv[last], dz1, lp1, ls1, V, err)
+    assert torch.equal(dz[last], dz1) and torch.equal(logps[last], lp1) and torch.equal(losses[last], ls1)
+    out = []
+    for rows, first in ((slice(0, N), N - n), (last, 0)):
+        dz.fill_(3.0)
+        seq, pair = torch.empty(4, device="cuda"), torch.empty(2, device="cuda")
+        start = i32([first, first, first + 90, first + 200, first + n - 7])
+        ws = torch.empty(gs.preference_loss_workspace(z[rows].shape[0], 2), dtype=torch.uint8, device="cuda")
+        gs.preference_loss(z[rows], t[rows], start, dz[rows], logps[rows], seq, pair, V, ws, err)
+        out.append((seq, pair, logps[last][:n - 7].clone(), dz[last].clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert bool((out[0][3][n - 7:] == 3.0).all()) and int(err.sum()) == 0
